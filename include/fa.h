@@ -100,6 +100,22 @@ int fa_forward_window(const void* q, const void* k, const void* v, void* o, floa
                       void* stream);
 
 /*
+ * fa_forward_sinks -- fa_forward_window with a few first keys ("sinks") that
+ * stay visible behind the window: query i sees key j iff j <= i + (Tk - Tq)
+ * and (j > i + (Tk - Tq) - window or j < sinks).  A model that streams past its
+ * window keeps its first tokens this way, because rows put much of their weight
+ * on them.  sinks = 0 gives fa_forward_window; sinks outside [0, 1024] is
+ * FA_ERR_INVALID_ARG.  Key tiles that hold neither sinks nor any key of a query
+ * tile's windows are not read.  Other arguments and errors as
+ * fa_forward_window.  Values of K and V have to be finite where any row of the
+ * same 128-row query tile sees them (a masked probability is 0, and 0 times a
+ * NaN or an infinity of V is NaN), as for the other prefill entry points.
+ */
+int fa_forward_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
+                     int B, int Hq, int Hkv, int Tq, int Tk, int d, float scale, int window,
+                     int sinks, void* stream);
+
+/*
  * fa_forward_dropout -- fa_forward with dropout on P fused into the kernel
  * ("Efficient attention: memory-bound", "Real code moves even more", lists
  * dropout among the elementwise steps on P before the final product):
@@ -195,6 +211,24 @@ int fa_backward_deterministic(const void* q, const void* k, const void* v, const
                               int causal, int window, void* stream);
 
 /*
+ * fa_backward_sinks -- gradients of fa_forward_sinks (the same window and
+ * sinks; o and lse from it).  A key tile that holds sinks is seen by every later
+ * query tile, so it is cut along the queries into pieces whose dK and dV are
+ * summed in fp32 in a fixed order.
+ *   deterministic  0: dQ by bulk reduce-adds as fa_backward; 1: dQ in a pass of
+ *                  its own as fa_backward_deterministic.
+ *   ws             at least fa_backward_sinks_workspace_bytes(): the workspace of
+ *                  fa_backward and the pieces' partial sums.
+ * Other arguments and errors as fa_backward_window.
+ */
+size_t fa_backward_sinks_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d, int window, int sinks);
+int fa_backward_sinks(const void* q, const void* k, const void* v, const void* o,
+                      const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                      void* ws, size_t ws_bytes,
+                      int B, int Hq, int Hkv, int Tq, int Tk, int d, float scale, int window,
+                      int sinks, int deterministic, void* stream);
+
+/*
  * The three steps fa_backward runs, in this order on one stream, exposed so
  * that a caller can schedule or time them separately.  They share the
  * workspace of fa_backward_workspace_bytes() and its layout; arguments mean
@@ -286,6 +320,19 @@ int fa_decode_splitkv_window(const void* q, const void* k_cache, const void* v_c
                              int window, void* stream);
 
 /*
+ * fa_decode_splitkv_sinks -- fa_decode_splitkv_window with the sinks of
+ * fa_forward_sinks: the query sees the last `window` cached keys and the first
+ * `sinks` of its sequence.  sinks = 0 gives fa_decode_splitkv_window; outside
+ * [0, 1024] it is FA_ERR_INVALID_ARG.  With sinks > 0, cache rows that the query
+ * does not see may hold anything, NaN included.  Other arguments, workspace and
+ * errors as fa_decode_splitkv_window.
+ */
+int fa_decode_splitkv_sinks(const void* q, const void* k_cache, const void* v_cache,
+                            const int* seqlens_k, void* o, float* lse, void* ws, size_t ws_bytes,
+                            int B, int Hq, int Hkv, int Tk_max, int d, float scale, int chunk,
+                            int window, int sinks, void* stream);
+
+/*
  * fa_decode_splitkv_noalloc -- fa_decode_splitkv for callers that cannot
  * allocate device memory where they call it: a plug-in interface of a
  * serving engine that hands the kernel its input and output tensors but no
@@ -358,6 +405,88 @@ int fa_decode_splitkv_partial(const void* q, const void* k_cache, const void* v_
  */
 int fa_decode_merge(const float* o_parts, size_t o_stride, const float* lse_parts, size_t lse_stride,
                     void* o, float* lse, int R, int B, int Hq, int d, void* stream);
+
+/*
+ * fa_rope -- rotary positions on q and k before attention: pair i of a head's
+ * first rotary_dim dims turns by theta = pos * freqs[i] and is scaled,
+ *   (x, y) -> amplitude (x cos theta - y sin theta, x sin theta + y cos theta);
+ * the dims behind rotary_dim are copied.
+ *   q, k        bf16 [B,T,Hq,d] and [B,T,Hkv,d], last dim contiguous; Hq or
+ *               Hkv may be 0 (the pointers are then not looked at)
+ *   q_out, k_out  bf16 outputs of the same shapes
+ *   strides     HOST array of 12: for q, q_out, k, k_out the strides of the
+ *               batch, token and head dims, in elements, each >= 0 and a multiple
+ *               of 8.  An input may be a slice of a packed projection or
+ *               broadcast; no two elements of an output may share their place.
+ *               An output is its own input (same pointer, same strides) or its
+ *               memory range is apart from it.
+ *   positions   DEVICE int32 [B,T], or NULL: row t has position t
+ *   freqs       DEVICE fp64 [rotary_dim / 2], radians per position.  Angles are
+ *               formed in 64 bits.
+ *   rotary_dim  a multiple of 16 in [16, d]
+ *   interleaved 0: pair i is dims (i, i + rotary_dim / 2); 1: (2i, 2i + 1)
+ * d must be 64 or 128.  B == 0 or T == 0 is a no-op.
+ *
+ * fa_rope_backward -- its gradient: dq, dk of the rotated tensors in, those of
+ * the unrotated ones out (the same turn by -theta).  Arguments as fa_rope.
+ */
+int fa_rope(const void* q, void* q_out, const void* k, void* k_out, const int64_t* strides,
+            const int* positions, const double* freqs, int rotary_dim, int interleaved, float amplitude,
+            int B, int T, int Hq, int Hkv, int d, void* stream);
+int fa_rope_backward(const void* dq, void* dq_out, const void* dk, void* dk_out, const int64_t* strides,
+                     const int* positions, const double* freqs, int rotary_dim, int interleaved, float amplitude,
+                     int B, int T, int Hq, int Hkv, int d, void* stream);
+
+/*
+ * The 4-bit KV cache: decode reads every cached key and value once, so bytes
+ * per key are its time.  A row of d values is held in groups of 32 dims, each
+ * with a bf16 step s and centre z:
+ *   s = bf16((max - min) / 15),  z = bf16(min + 8 s),
+ *   code = clamp(round((x - z) / s), -8, 7) + 8 (8 where s = 0),
+ *   value = z + s (code - 8),
+ * 160 bytes for a key and its value at d = 128 (bf16: 512).  A group that holds
+ * a NaN or an infinity reads back non-finite.  The cache's four buffers, all
+ * 16-byte aligned, rows of one sequence and KV head contiguous:
+ *   k_codes, v_codes    uint8 [B][Hkv][Tk_max][d/2], dim 2i in the low and dim
+ *                       2i + 1 in the high nibble of byte i
+ *   k_params, v_params  bf16 [B][Hkv][Tk_max][2 d/32]: the row's steps, then its
+ *                       centres
+ * Tk_max must be a multiple of 64, d 64 or 128.  Offsets are 64-bit.
+ *
+ * fa_kv4_append -- rows k, v bf16 [B,T,Hkv,d] (last dim contiguous; `strides` a
+ * HOST array of 6: batch, token and head stride of k, then of v, in elements,
+ * each >= 0 and a multiple of 8) into the cache at positions start[b] + t.
+ *   start  DEVICE int32 [B];  count  DEVICE int32 [B], rows of sequence b that
+ *          are written (t < count[b]), or NULL: all T.
+ * Rows at positions outside [0, Tk_max) are dropped; nothing else is written.
+ *
+ * fa_kv4_read -- the values at positions start[b] + t, rounded to bf16, as dense
+ * k, v [B,T,Hkv,d] (a prefill's keys, for instance).  Rows t >= count[b], or
+ * outside [0, Tk_max), read as zeros.
+ */
+int fa_kv4_append(const void* k, const void* v, const int64_t* strides, void* k_codes, void* k_params,
+                  void* v_codes, void* v_params, const int* start, const int* count,
+                  int B, int T, int Hkv, int Tk_max, int d, void* stream);
+int fa_kv4_read(void* k, void* v, const void* k_codes, const void* k_params, const void* v_codes,
+                const void* v_params, const int* start, const int* count,
+                int B, int T, int Hkv, int Tk_max, int d, void* stream);
+
+/*
+ * fa_kv4_decode -- fa_decode_splitkv over the 4-bit cache.
+ *   q [B,Hq,d] bf16; seqlens_k DEVICE int32 [B], read clamped to [0, Tk_max];
+ *   o [B,Hq,d] bf16, lse [B,Hq] fp32 out;
+ *   window  0: every key of the sequence; >= 1: the last `window` keys;
+ *   sinks   in [0, 1024]: with a window, the first `sinks` keys as well (without
+ *           one, sinks > 0 is FA_ERR_INVALID_ARG);
+ *   ws/ws_bytes  at least fa_kv4_decode_workspace_bytes(); contents on entry do
+ *           not matter.
+ * Hq/Hkv must be 1, 2, 4 or 8.  Rows that the query does not see may hold
+ * anything.  The same inputs give the same bits.
+ */
+size_t fa_kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int Tk_max, int d);
+int fa_kv4_decode(const void* q, const void* k_codes, const void* k_params, const void* v_codes,
+                  const void* v_params, const int* seqlens_k, void* o, float* lse, void* ws, size_t ws_bytes,
+                  int B, int Hq, int Hkv, int Tk_max, int d, float scale, int window, int sinks, void* stream);
 
 /*
  * fa_check -- synchronise `stream`, then read and clear the device status

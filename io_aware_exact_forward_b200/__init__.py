@@ -25,3 +25,12 @@ from ._binding import (  # noqa: F401
     selftest_bounded_wait,
 )
 from .context_parallel import decode_splitkv_cp  # noqa: F401,E402
+from .kv4 import (  # noqa: F401,E402
+    KV4Cache,
+    kv4_append,
+    kv4_cache,
+    kv4_decode,
+    kv4_decode_workspace_bytes,
+    kv4_read,
+)
+from .rope import rope, rope_backward, rope_frequencies  # noqa: F401,E402

@@ -8,6 +8,7 @@ exception is raised.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -57,6 +58,16 @@ SIGNATURES = {
     "fa_decode_splitkv_noalloc": (_c_int, [_vp] * 6 + [_c_int] * 5 + [_c_float, _c_int, _vp]),
     "fa_decode_splitkv_partial": (_c_int, [_vp] * 6 + [_vp, _c_size] + [_c_int] * 5 + [_c_float, _c_int, _vp]),
     "fa_decode_merge": (_c_int, [_vp, _c_size, _vp, _c_size, _vp, _vp] + [_c_int] * 4 + [_vp]),
+    "fa_forward_sinks": (_c_int, [_vp] * 5 + [_c_int] * 6 + [_c_float, _c_int, _c_int, _vp]),
+    "fa_backward_sinks_workspace_bytes": (_c_size, [_c_int] * 8),
+    "fa_backward_sinks": (_c_int, [_vp] * 9 + [_vp, _c_size] + [_c_int] * 6 + [_c_float] + [_c_int] * 3 + [_vp]),
+    "fa_decode_splitkv_sinks": (_c_int, [_vp] * 6 + [_vp, _c_size] + [_c_int] * 5 + [_c_float] + [_c_int] * 3 + [_vp]),
+    "fa_rope": (_c_int, [_vp] * 7 + [_c_int] * 2 + [_c_float] + [_c_int] * 5 + [_vp]),
+    "fa_rope_backward": (_c_int, [_vp] * 7 + [_c_int] * 2 + [_c_float] + [_c_int] * 5 + [_vp]),
+    "fa_kv4_append": (_c_int, [_vp] * 9 + [_c_int] * 5 + [_vp]),
+    "fa_kv4_read": (_c_int, [_vp] * 8 + [_c_int] * 5 + [_vp]),
+    "fa_kv4_decode_workspace_bytes": (_c_size, [_c_int] * 5),
+    "fa_kv4_decode": (_c_int, [_vp] * 8 + [_vp, _c_size] + [_c_int] * 5 + [_c_float] + [_c_int] * 2 + [_vp]),
     "fa_check": (_c_int, [_vp]),
     "fa_selftest_bounded_wait": (_c_int, [_c_int, _vp]),
     "fa_selftest_exp2_poly": (_c_int, [_vp, _vp, _c_int, _vp]),
@@ -115,11 +126,26 @@ def _raise(fn, st):
         raise FAError(fn, st)
 
 
-def forward(q, k, v, scale=None, causal=False, out=None, lse=None, window=None):
+def _need_window(window, sinks):
+    if sinks and window is None:
+        raise ValueError("sinks need a window (without one every key is visible)")
+
+
+def _on_device(device):
+    """Guard that makes ``device`` the current one where it is not: a launch on
+    another device's stream fails, and kernel attributes are per device."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def forward(q, k, v, scale=None, causal=False, out=None, lse=None, window=None, sinks=0):
     """O, LSE = attention(q, k, v).  q [B,Tq,Hq,d], k/v [B,Tk,Hkv,d] bf16 (CUDA).
     ``window`` (int >= 1) selects the sliding-window mask of fa_forward_window
-    (which includes the causal one)."""
+    (which includes the causal one); ``sinks`` first keys stay visible behind it
+    (fa_forward_sinks)."""
     lib = load_library()
+    _need_window(window, sinks)
     B, Tq, Hq, d = q.shape
     Tk, Hkv = k.shape[1], k.shape[2]
     dev = q.device
@@ -137,11 +163,28 @@ def forward(q, k, v, scale=None, causal=False, out=None, lse=None, window=None):
         st = lib.fa_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Tq, Tk, d,
                             float(scale), int(bool(causal)), _stream_ptr(dev))
         _raise("fa_forward", st)
+    elif sinks:
+        _check_kv_shapes(q, k, v)
+        with _on_device(dev):
+            st = lib.fa_forward_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Tq, Tk, d,
+                                      float(scale), int(window), int(sinks), _stream_ptr(dev))
+        _raise("fa_forward_sinks", st)
     else:
         st = lib.fa_forward_window(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Tq, Tk, d,
                                    float(scale), int(window), _stream_ptr(dev))
         _raise("fa_forward_window", st)
     return out, lse
+
+
+def _check_kv_shapes(q, k, v):
+    want = (q.shape[0], k.shape[1], k.shape[2], q.shape[-1])
+    if tuple(k.shape) != want or tuple(v.shape) != want:
+        raise ValueError(f"k and v must be {want}, got {tuple(k.shape)} and {tuple(v.shape)}")
+
+
+def _check_out(name, t, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def forward_dropout(q, k, v, p_drop, seed, offset=0, scale=None, causal=False, out=None, lse=None):
@@ -200,12 +243,14 @@ def backward_workspace_bytes(B, Hq, Hkv, Tq, Tk, d) -> int:
 
 
 def backward(q, k, v, o, lse, do, scale=None, causal=False, workspace=None, dq=None, dk=None, dv=None,
-             window=None, deterministic=False):
+             window=None, deterministic=False, sinks=0):
     """dQ, dK, dV for L = sum(dO * O).  `workspace` (uint8 CUDA tensor) is
     allocated here when not given; ``window`` as in forward().
     ``deterministic``: fa_backward_deterministic (dQ the same bit for bit from
-    run to run, at the cost of a second pass)."""
+    run to run, at the cost of a second pass).  ``sinks`` as in forward()
+    (fa_backward_sinks)."""
     lib = load_library()
+    _need_window(window, sinks)
     B, Tq, Hq, d = q.shape
     Tk, Hkv = k.shape[1], k.shape[2]
     dev = q.device
@@ -214,7 +259,10 @@ def backward(q, k, v, o, lse, do, scale=None, causal=False, workspace=None, dq=N
     _check_dev("lse", lse, torch.float32, dev)
     if scale is None:
         scale = d ** -0.5
-    need = backward_workspace_bytes(B, Hq, Hkv, Tq, Tk, d)
+    if sinks:
+        need = int(lib.fa_backward_sinks_workspace_bytes(B, Hq, Hkv, Tq, Tk, d, int(window), int(sinks)))
+    else:
+        need = backward_workspace_bytes(B, Hq, Hkv, Tq, Tk, d)
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     dq = torch.empty_like(q) if dq is None else dq
@@ -222,7 +270,16 @@ def backward(q, k, v, o, lse, do, scale=None, causal=False, workspace=None, dq=N
     dv = torch.empty_like(v) if dv is None else dv
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv),
             _ptr(workspace), workspace.numel(), B, Hq, Hkv, Tq, Tk, d, float(scale))
-    if deterministic:
+    if sinks:
+        _check_kv_shapes(q, k, v)
+        for n, t, like in (("o", o, q), ("do", do, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+            _check_dev(n, t, torch.bfloat16, dev)
+            _check_out(n, t, like.shape)
+        _check_out("lse", lse, (B, Hq, Tq))
+        with _on_device(dev):
+            st = lib.fa_backward_sinks(*args, int(window), int(sinks), int(bool(deterministic)), _stream_ptr(dev))
+        _raise("fa_backward_sinks", st)
+    elif deterministic:
         win = 0 if window is None else int(window)
         st = lib.fa_backward_deterministic(*args, int(bool(causal) or win > 0), win, _stream_ptr(dev))
         _raise("fa_backward_deterministic", st)
@@ -268,10 +325,12 @@ def decode_workspace_bytes(B, Hq, Tk_max, d, chunk=256) -> int:
 
 
 def decode_splitkv(q, k_cache, v_cache, seqlens, scale=None, chunk=256, workspace=None, out=None, lse=None,
-                   window=None):
+                   window=None, sinks=0):
     """Split-KV decode.  q [B,Hq,d], caches [B,Tk_max,Hkv,d] bf16, seqlens int32 [B] (CUDA).
-    ``window`` (int >= 1) keeps only the last `window` keys of each sequence."""
+    ``window`` (int >= 1) keeps only the last `window` keys of each sequence, and
+    ``sinks`` its first ones with them (fa_decode_splitkv_sinks)."""
     lib = load_library()
+    _need_window(window, sinks)
     B, Hq, d = q.shape
     Tk_max, Hkv = k_cache.shape[1], k_cache.shape[2]
     dev = q.device
@@ -290,10 +349,24 @@ def decode_splitkv(q, k_cache, v_cache, seqlens, scale=None, chunk=256, workspac
     if window is None:
         st = lib.fa_decode_splitkv(*args, _stream_ptr(dev))
         _raise("fa_decode_splitkv", st)
+    elif sinks:
+        _check_kv_shapes(q, k_cache, v_cache)
+        _check_decode_out(q, seqlens, out, lse)
+        with _on_device(dev):
+            st = lib.fa_decode_splitkv_sinks(*args, int(window), int(sinks), _stream_ptr(dev))
+        _raise("fa_decode_splitkv_sinks", st)
     else:
         st = lib.fa_decode_splitkv_window(*args, int(window), _stream_ptr(dev))
         _raise("fa_decode_splitkv_window", st)
     return out, lse
+
+
+def _check_decode_out(q, seqlens, out, lse):
+    _check_dev("out", out, torch.bfloat16, q.device)
+    _check_dev("lse", lse, torch.float32, q.device)
+    _check_out("out", out, q.shape)
+    _check_out("lse", lse, q.shape[:2])
+    _check_out("seqlens", seqlens, q.shape[:1])
 
 
 def decode_splitkv_noalloc(q, k_cache, v_cache, seqlens, scale=None, chunk=256, out=None, lse=None):

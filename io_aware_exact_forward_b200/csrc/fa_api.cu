@@ -17,6 +17,8 @@
 #include "fa_bwd.cuh"
 #include "fa_bwd_dq.cuh"
 #include "fa_decode.cuh"
+#include "fa_rope.cuh"
+#include "fa_kv4.cuh"
 
 namespace fa {
 
@@ -100,19 +102,20 @@ static int set_smem(Fn* kernel, int bytes) {
 // the split adds up only if the block is launched with exactly the per-thread
 // count it was planned for (an increase beyond the launch's pool would wait
 // forever), so a build that came out differently is refused, not launched.
-template <int D, bool F8, bool DROP>
+template <int D, bool F8, bool DROP, bool SINK = false>
 static int fwd_setup_one() {
   using C = FwdCfg<D, F8, DROP>;
   cudaFuncAttributes a;
-  if (cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(fa_fwd_kernel<D, F8, DROP>)) != cudaSuccess)
+  if (cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(fa_fwd_kernel<D, F8, DROP, SINK>)) != cudaSuccess)
     return FA_ERR_CUDA;
   if (a.numRegs != C::REG_LAUNCH) return FA_ERR_UNSUPPORTED;
-  return set_smem(fa_fwd_kernel<D, F8, DROP>, C::SMEM_BYTES);
+  return set_smem(fa_fwd_kernel<D, F8, DROP, SINK>, C::SMEM_BYTES);
 }
 
 template <int D, int G>
 static int decode_setup_one() {
   int st = set_smem(fa_decode_split_kernel<D, G>, DecCfg<D, G>::SMEM_BYTES);
+  if (!st) st = set_smem(fa_decode_split_kernel<D, G, true>, DecCfg<D, G>::SMEM_BYTES);
   return st;
 }
 
@@ -143,6 +146,8 @@ static int device_setup_impl() {
   if (!st) st = fwd_setup_one<128, true, false>();
   if (!st) st = fwd_setup_one<64, false, true>();
   if (!st) st = fwd_setup_one<128, false, true>();
+  if (!st) st = fwd_setup_one<64, false, false, true>();
+  if (!st) st = fwd_setup_one<128, false, false, true>();
   if (!st) st = bwd_setup();
   if (!st) st = bwd_dq_setup();
   if (!st) st = decode_setup();
@@ -198,6 +203,9 @@ static int check_prefill(int B, int Hq, int Hkv, int Tq, int Tk, int d, float sc
   return FA_OK;
 }
 
+// Sinks are a few first tokens; the limit bounds the backward's partial sums.
+static constexpr int kMaxSinks = 1024;
+
 }  // namespace fa
 
 using namespace fa;
@@ -237,11 +245,12 @@ static uint32_t keep_threshold(float p_drop) {
 static int forward_impl(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
                         int Hkv, int Tq, int Tk, int d, float scale, int causal, int window, void* stream,
                         bool f8 = false, float qk_factor = 1.f, float o_scale = 1.f, uint32_t drop_t = 256,
-                        uint32_t seed_lo = 0, uint32_t seed_hi = 0, uint32_t drop_offset = 0) {
+                        uint32_t seed_lo = 0, uint32_t seed_hi = 0, uint32_t drop_offset = 0, int sinks = 0) {
   const bool drop = drop_t < 256;
   int st = check_prefill(B, Hq, Hkv, Tq, Tk, d, scale, causal);
   if (st) return st;
   if (window < 0 || window > (1 << 30)) return FA_ERR_INVALID_ARG;
+  if (sinks < 0 || sinks > kMaxSinks) return FA_ERR_INVALID_ARG;
   if (f8 && d != 128) return FA_ERR_UNSUPPORTED;
   if (B == 0 || Tq == 0) return FA_OK;
   if (!q || !o || !lse || (Tk > 0 && (!k || !v))) return FA_ERR_INVALID_ARG;
@@ -261,6 +270,7 @@ static int forward_impl(const void* q, const void* k, const void* v, void* o, fl
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Tq = Tq; p.Tk = Tk;
   p.causal = causal;
   p.window = window;
+  p.sinks = sinks;
   p.scale_log2 = scale * qk_factor * 1.4426950408889634f;
   p.o_scale = o_scale;
   p.drop_t = drop_t;
@@ -284,6 +294,10 @@ static int forward_impl(const void* q, const void* k, const void* v, void* o, fl
     fa_fwd_kernel<64, false, true><<<grid, FwdCfg<64, false, true>::THREADS, FwdCfg<64, false, true>::SMEM_BYTES, s>>>(p);
   else if (drop)
     fa_fwd_kernel<128, false, true><<<grid, FwdCfg<128, false, true>::THREADS, FwdCfg<128, false, true>::SMEM_BYTES, s>>>(p);
+  else if (sinks > 0 && d == 64)
+    fa_fwd_kernel<64, false, false, true><<<grid, FwdCfg<64>::THREADS, FwdCfg<64>::SMEM_BYTES, s>>>(p);
+  else if (sinks > 0)
+    fa_fwd_kernel<128, false, false, true><<<grid, FwdCfg<128>::THREADS, FwdCfg<128>::SMEM_BYTES, s>>>(p);
   else if (d == 64)
     fa_fwd_kernel<64><<<grid, FwdCfg<64>::THREADS, FwdCfg<64>::SMEM_BYTES, s>>>(p);
   else
@@ -302,6 +316,13 @@ int fa_forward_window(const void* q, const void* k, const void* v, void* o, floa
                       int Hkv, int Tq, int Tk, int d, float scale, int window, void* stream) {
   if (window < 1) return FA_ERR_INVALID_ARG;
   return forward_impl(q, k, v, o, lse, B, Hq, Hkv, Tq, Tk, d, scale, 1, window, stream);
+}
+
+int fa_forward_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
+                     int Tq, int Tk, int d, float scale, int window, int sinks, void* stream) {
+  if (window < 1) return FA_ERR_INVALID_ARG;
+  return forward_impl(q, k, v, o, lse, B, Hq, Hkv, Tq, Tk, d, scale, 1, window, stream, false, 1.f, 1.f, 256, 0, 0, 0,
+                      sinks);
 }
 
 int fa_forward_dropout(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq,
@@ -362,6 +383,30 @@ static int check_ptrs(std::initializer_list<const void*> ptrs) {
   return FA_OK;
 }
 
+// How the backward cuts up the key tiles that hold sinks (see BwdParams): a
+// piece is about as many query tiles as a windowed key tile sees, so that no
+// item outlasts the others by far; at most 32 pieces, so that the partial sums
+// stay small beside the fp32 dQ accumulator.
+struct SinkPlan {
+  int tiles, pieces;
+  size_t part_bytes;
+};
+static SinkPlan sink_plan(int B, int Hkv, int Tq, int Tk, int d, int window, int sinks) {
+  SinkPlan s;
+  s.tiles = (std::min(sinks, Tk) + 127) / 128;
+  const int n_qt = (Tq + 127) / 128;
+  const int per = std::max(4, (int)(((long long)window + 127) / 128) + 1);
+  s.pieces = std::min(32, std::max(1, (n_qt + per - 1) / per));
+  s.part_bytes = s.pieces > 1 ? round256((size_t)B * Hkv * s.tiles * s.pieces * 2 * 128 * d * 4) : 0;
+  return s;
+}
+
+size_t fa_backward_sinks_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d, int window, int sinks) {
+  const size_t base = fa_backward_workspace_bytes(B, Hq, Hkv, Tq, Tk, d);
+  if (base == 0 || Hkv < 1 || Tk < 0 || window < 1 || sinks < 0 || sinks > kMaxSinks) return base;
+  return base + sink_plan(B, Hkv, Tq, Tk, d, window, sinks).part_bytes;
+}
+
 // zero_acc = false leaves the fp32 dQ accumulator alone (a backward whose dQ
 // pass writes dq directly does not read it).
 static int preprocess_impl(const void* o, const float* lse, const void* dO, void* ws, size_t ws_bytes, int B,
@@ -402,7 +447,7 @@ int fa_backward_preprocess(const void* o, const float* lse, const void* dO, void
 static int dkdv_impl(const void* q, const void* k, const void* v, const void* dO, void* dk, void* dv, void* ws,
                      size_t ws_bytes, int B, int Hq, int Hkv, int Tq, int Tk, int d, float scale, int causal,
                      int window, void* stream, uint32_t drop_t = 256, uint32_t seed_lo = 0, uint32_t seed_hi = 0,
-                     uint32_t drop_offset = 0, bool det = false, void* dq_out = nullptr) {
+                     uint32_t drop_offset = 0, bool det = false, void* dq_out = nullptr, int sinks = 0) {
   const bool drop = drop_t < 256;
   int st = check_prefill(B, Hq, Hkv, Tq, Tk, d, scale, causal);
   if (st) return st;
@@ -435,6 +480,18 @@ static int dkdv_impl(const void* q, const void* k, const void* v, const void* dO
   p.scale_log2 = scale * 1.4426950408889634f;
   p.n_kv_tiles = (Tk + 127) / 128;
   p.n_items = p.n_kv_tiles * B * Hkv;
+  if (sinks > 0) {
+    const SinkPlan sp = sink_plan(B, Hkv, Tq, Tk, d, window, sinks);
+    if (ws_bytes < fa_backward_sinks_workspace_bytes(B, Hq, Hkv, Tq, Tk, d, window, sinks)) return FA_ERR_WORKSPACE;
+    const long long items = (long long)B * Hkv * (p.n_kv_tiles + (long long)sp.tiles * (sp.pieces - 1));
+    if (items > 0x7FFFFFFFll) return FA_ERR_INVALID_ARG;
+    p.n_items = (int)items;
+    p.sinks = sinks;
+    p.n_sink_tiles = sp.tiles;
+    p.pieces = sp.pieces;
+    p.sink_part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) +
+                                           fa_backward_workspace_bytes(B, Hq, Hkv, Tq, Tk, d));
+  }
   p.drop_t = drop_t;
   p.seed_lo = seed_lo;
   p.seed_hi = seed_hi;
@@ -458,7 +515,25 @@ static int dkdv_impl(const void* q, const void* k, const void* v, const void* dO
       fa_bwd_dkdv_kernel<128, false, true><<<grid, BwdCfg<128, true>::THREADS, BwdCfg<128, true>::SMEM_BYTES, s>>>(p);
     return launch_status();
   }
+  // dK and dV of cut-up sink tiles, once their pieces are done
+  auto sum_sinks = [&]() -> int {
+    if (sinks == 0 || p.pieces == 1) return FA_OK;
+    const dim3 g((unsigned)(B * Hkv * p.n_sink_tiles), 2);
+    if (d == 64)
+      fa_bwd_sink_sum_kernel<64><<<g, 256, 0, s>>>(p.sink_part, p.dk, p.dv, Hkv, Tk, p.n_sink_tiles, p.pieces);
+    else
+      fa_bwd_sink_sum_kernel<128><<<g, 256, 0, s>>>(p.sink_part, p.dk, p.dv, Hkv, Tk, p.n_sink_tiles, p.pieces);
+    return launch_status();
+  };
   if (!det) {
+    if (sinks > 0) {
+      if (d == 64)
+        fa_bwd_dkdv_kernel<64, 2><<<grid, BwdCfg<64>::THREADS, BwdCfg<64>::SMEM_BYTES, s>>>(p);
+      else
+        fa_bwd_dkdv_kernel<128, 2><<<grid, BwdCfg<128>::THREADS, BwdCfg<128>::SMEM_BYTES, s>>>(p);
+      if ((st = launch_status())) return st;
+      return sum_sinks();
+    }
     if (d == 64 && window > 0)
       fa_bwd_dkdv_kernel<64, true><<<grid, BwdCfg<64>::THREADS, BwdCfg<64>::SMEM_BYTES, s>>>(p);
     else if (d == 64)
@@ -472,7 +547,11 @@ static int dkdv_impl(const void* q, const void* k, const void* v, const void* dO
   // deterministic: dK/dV without dQ, then the dQ pass
   using C64 = BwdCfg<64, false, false>;
   using C128 = BwdCfg<128, false, false>;
-  if (d == 64 && window > 0)
+  if (sinks > 0 && d == 64)
+    fa_bwd_dkdv_kernel<64, 2, false, false><<<grid, C64::THREADS, C64::SMEM_BYTES, s>>>(p);
+  else if (sinks > 0)
+    fa_bwd_dkdv_kernel<128, 2, false, false><<<grid, C128::THREADS, C128::SMEM_BYTES, s>>>(p);
+  else if (d == 64 && window > 0)
     fa_bwd_dkdv_kernel<64, true, false, false><<<grid, C64::THREADS, C64::SMEM_BYTES, s>>>(p);
   else if (d == 64)
     fa_bwd_dkdv_kernel<64, false, false, false><<<grid, C64::THREADS, C64::SMEM_BYTES, s>>>(p);
@@ -481,6 +560,7 @@ static int dkdv_impl(const void* q, const void* k, const void* v, const void* dO
   else
     fa_bwd_dkdv_kernel<128, false, false, false><<<grid, C128::THREADS, C128::SMEM_BYTES, s>>>(p);
   if ((st = launch_status())) return st;
+  if ((st = sum_sinks())) return st;
   if (Tq == 0) return FA_OK;
   DqParams qp;
   memset(&qp, 0, sizeof(qp));
@@ -494,6 +574,7 @@ static int dkdv_impl(const void* q, const void* k, const void* v, const void* dO
   qp.dq = reinterpret_cast<__nv_bfloat16*>(dq_out);
   qp.B = B; qp.Hq = Hq; qp.Hkv = Hkv; qp.Tq = Tq; qp.Tk = Tk; qp.causal = causal;
   qp.window = window;
+  qp.sinks = sinks;
   qp.Tq_pad = p.Tq_pad;
   qp.scale = scale;
   qp.scale_log2 = p.scale_log2;
@@ -503,7 +584,11 @@ static int dkdv_impl(const void* q, const void* k, const void* v, const void* dO
   qp.n_items = (int)n_items;
   qp.wait_limit_ns = kWaitLimitNs;
   const unsigned nblk = (unsigned)qp.n_items;
-  if (d == 64 && window > 0)
+  if (sinks > 0 && d == 64)
+    fa_bwd_dq_kernel<64, 2><<<nblk, DqCfg<64>::THREADS, DqCfg<64>::SMEM_BYTES, s>>>(qp);
+  else if (sinks > 0)
+    fa_bwd_dq_kernel<128, 2><<<nblk, DqCfg<128>::THREADS, DqCfg<128>::SMEM_BYTES, s>>>(qp);
+  else if (d == 64 && window > 0)
     fa_bwd_dq_kernel<64, true><<<nblk, DqCfg<64>::THREADS, DqCfg<64>::SMEM_BYTES, s>>>(qp);
   else if (d == 64)
     fa_bwd_dq_kernel<64, false><<<nblk, DqCfg<64>::THREADS, DqCfg<64>::SMEM_BYTES, s>>>(qp);
@@ -560,20 +645,23 @@ static int backward_impl(const void* q, const void* k, const void* v, const void
                          const void* dO, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, int B, int Hq,
                          int Hkv, int Tq, int Tk, int d, float scale, int causal, int window, void* stream,
                          uint32_t drop_t = 256, uint32_t seed_lo = 0, uint32_t seed_hi = 0,
-                         uint32_t drop_offset = 0, bool det = false) {
+                         uint32_t drop_offset = 0, bool det = false, int sinks = 0) {
   int st = check_prefill(B, Hq, Hkv, Tq, Tk, d, scale, causal);
   if (st) return st;
   if (window < 0 || window > (1 << 30)) return FA_ERR_INVALID_ARG;
+  if (sinks < 0 || sinks > kMaxSinks) return FA_ERR_INVALID_ARG;
   if (B == 0 || (Tq == 0 && Tk == 0)) return FA_OK;
   if (Tq > 0 && (st = check_ptrs({q, o, lse, dO, dq}))) return st;
   if (Tk > 0 && (st = check_ptrs({k, v, dk, dv}))) return st;
   if ((st = check_ws(ws, ws_bytes, B, Hq, Hkv, Tq, Tk, d))) return st;
+  if (sinks > 0 && ws_bytes < fa_backward_sinks_workspace_bytes(B, Hq, Hkv, Tq, Tk, d, window, sinks))
+    return FA_ERR_WORKSPACE;
   // deterministic: the dQ pass writes dq itself (when there are keys; with
   // none, dq is the zeroed accumulator converted)
   const bool direct = det && Tq > 0 && Tk > 0;
   if ((st = preprocess_impl(o, lse, dO, ws, ws_bytes, B, Hq, Hkv, Tq, Tk, d, stream, !direct))) return st;
   if ((st = dkdv_impl(q, k, v, dO, dk, dv, ws, ws_bytes, B, Hq, Hkv, Tq, Tk, d, scale, causal, window, stream,
-                      drop_t, seed_lo, seed_hi, drop_offset, det, direct ? dq : nullptr)))
+                      drop_t, seed_lo, seed_hi, drop_offset, det, direct ? dq : nullptr, sinks)))
     return st;
   if (direct) return FA_OK;
   return fa_backward_dq_finalize(dq, ws, ws_bytes, B, Hq, Hkv, Tq, Tk, d, stream);
@@ -615,6 +703,14 @@ int fa_backward_deterministic(const void* q, const void* k, const void* v, const
                        stream, 256, 0, 0, 0, true);
 }
 
+int fa_backward_sinks(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                      void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, int B, int Hq, int Hkv, int Tq, int Tk,
+                      int d, float scale, int window, int sinks, int deterministic, void* stream) {
+  if (window < 1 || (deterministic != 0 && deterministic != 1)) return FA_ERR_INVALID_ARG;
+  return backward_impl(q, k, v, o, lse, dO, dq, dk, dv, ws, ws_bytes, B, Hq, Hkv, Tq, Tk, d, scale, 1, window, stream,
+                       256, 0, 0, 0, deterministic != 0, sinks);
+}
+
 static size_t decode_nchunk(int Tk_max, int chunk) { return ((size_t)Tk_max + chunk - 1) / chunk; }
 
 size_t fa_decode_workspace_bytes(int B, int Hq, int Tk_max, int d, int chunk) {
@@ -628,10 +724,11 @@ size_t fa_decode_workspace_bytes(int B, int Hq, int Tk_max, int d, int chunk) {
 // `o` receives bf16 O, or, when `o32` is non-null instead, fp32 O.
 static int decode_impl(const void* q, const void* k_cache, const void* v_cache, const int* seqlens_k, void* o,
                        float* o32, float* lse, void* ws, size_t ws_bytes, int B, int Hq, int Hkv, int Tk_max,
-                       int d, float scale, int chunk, int window, void* stream) {
+                       int d, float scale, int chunk, int window, void* stream, int sinks = 0) {
   if (B < 0 || Hq < 1 || Hkv < 1 || Tk_max < 0 || Hq % Hkv != 0 || !isfinite(scale))
     return FA_ERR_INVALID_ARG;
   if (window < 0 || window > (1 << 30)) return FA_ERR_INVALID_ARG;
+  if (sinks < 0 || sinks > kMaxSinks) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   const int G = Hq / Hkv;
   if (G != 1 && G != 2 && G != 4 && G != 8) return FA_ERR_UNSUPPORTED;
@@ -651,7 +748,11 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache, 
   if (st) return st;
   DecodeParams p;
   memset(&p, 0, sizeof(p));
-  const size_t n = decode_nchunk(Tk_max, chunk);
+  size_t n = decode_nchunk(Tk_max, chunk);
+  // with sinks, only the visible chunks are items: those that hold sinks and
+  // those that a window can touch
+  if (sinks > 0)
+    n = std::min(n, (size_t)(sinks + chunk - 1) / chunk + ((size_t)window + chunk - 2) / chunk + 1);
   if (Tk_max > 0) {
     st = make_tmap_4d(&p.tm_k, k_cache, d, Hkv, Tk_max, B, 64, 64, true);
     if (!st) st = make_tmap_4d(&p.tm_v, v_cache, d, Hkv, Tk_max, B, 64, 64, true);
@@ -668,6 +769,7 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache, 
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Tk_max = Tk_max; p.chunk = chunk; p.nchunk = (int)n;
   p.n_items = (int)((size_t)B * Hkv * n);
   p.window = window;
+  p.sinks = sinks;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = kWaitLimitNs;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -676,8 +778,9 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache, 
     if ((st = sm_count(&nsm))) return st;
     // persistent: two CTAs per SM walk the (sequence, KV head, chunk) items
     dim3 grid((unsigned)std::min<long long>(p.n_items, (long long)kDecodeCtasPerSm * nsm));
-#define FA_DEC_LAUNCH(DD, GG) \
-    fa_decode_split_kernel<DD, GG><<<grid, DecCfg<DD, GG>::THREADS, DecCfg<DD, GG>::SMEM_BYTES, s>>>(p)
+#define FA_DEC_LAUNCH(DD, GG)                                                                             \
+    (sinks > 0 ? fa_decode_split_kernel<DD, GG, true><<<grid, DecCfg<DD, GG>::THREADS, DecCfg<DD, GG>::SMEM_BYTES, s>>>(p) \
+               : fa_decode_split_kernel<DD, GG><<<grid, DecCfg<DD, GG>::THREADS, DecCfg<DD, GG>::SMEM_BYTES, s>>>(p))
     if (d == 64) {
       if (G == 1) FA_DEC_LAUNCH(64, 1); else if (G == 2) FA_DEC_LAUNCH(64, 2);
       else if (G == 4) FA_DEC_LAUNCH(64, 4); else FA_DEC_LAUNCH(64, 8);
@@ -690,6 +793,13 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache, 
   }
   const int warps = B * Hq;
   const int blocks = (warps * 32 + 255) / 256;
+  if (sinks > 0) {
+    if (d == 64)
+      fa_decode_combine_kernel<64, true><<<blocks, 256, 0, s>>>(p);
+    else
+      fa_decode_combine_kernel<128, true><<<blocks, 256, 0, s>>>(p);
+    return launch_status();
+  }
   if (Tk_max > 0) {
     if (d == 64)
       fa_decode_combine_kernel<64><<<blocks, 256, 0, s>>>(p);
@@ -756,6 +866,14 @@ int fa_decode_splitkv_window(const void* q, const void* k_cache, const void* v_c
   if (window < 1) return FA_ERR_INVALID_ARG;
   return decode_impl(q, k_cache, v_cache, seqlens_k, o, nullptr, lse, ws, ws_bytes, B, Hq, Hkv, Tk_max, d, scale,
                      chunk, window, stream);
+}
+
+int fa_decode_splitkv_sinks(const void* q, const void* k_cache, const void* v_cache, const int* seqlens_k, void* o,
+                            float* lse, void* ws, size_t ws_bytes, int B, int Hq, int Hkv, int Tk_max, int d,
+                            float scale, int chunk, int window, int sinks, void* stream) {
+  if (window < 1) return FA_ERR_INVALID_ARG;
+  return decode_impl(q, k_cache, v_cache, seqlens_k, o, nullptr, lse, ws, ws_bytes, B, Hq, Hkv, Tk_max, d, scale,
+                     chunk, window, stream, sinks);
 }
 
 int fa_check(void* stream) {
@@ -873,4 +991,290 @@ extern "C" int fa_decode_splitkv_noalloc(const void* q, const void* k_cache, con
   // of the same call, so nothing in the scratch needs clearing.
   return fa_decode_splitkv(q, k_cache, v_cache, seqlens_k, o, lse, scratch, kDecodeScratchBytes, B, Hq, Hkv,
                            Tk_max, d, scale, chunk, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Rotary positions
+// ---------------------------------------------------------------------------
+namespace fa {
+
+// The layout [B][T][H][d] with these strides: every element its own place.
+static bool rope_dense_enough(const int64_t* st, int B, int T, int H, int d) {
+  struct Dim { int64_t stride, size; } dim[3] = {{st[0], B}, {st[1], T}, {st[2], H}};
+  std::sort(dim, dim + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  int64_t extent = d;
+  for (const Dim& m : dim) {
+    if (m.size < 2) continue;
+    if (m.stride < extent) return false;
+    extent = m.stride * (m.size - 1) + extent;
+  }
+  return true;
+}
+
+static int64_t rope_extent(const int64_t* st, int B, int T, int H, int d) {
+  return st[0] * (B - 1) + st[1] * (T - 1) + st[2] * (H - 1) + d;
+}
+
+// Checks one tensor and its output (strides st[0..2] and st[3..5]).
+static int rope_tensor(RopeTensor* r, const void* x, void* y, const int64_t* st, const int64_t* so, int B, int T,
+                       int H, int d) {
+  if (!x || !y) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    // 2^40 elements per step, so that offsets cannot leave 64 bits
+    if (st[i] < 0 || so[i] < 0 || st[i] > (1ll << 40) || so[i] > (1ll << 40)) return FA_ERR_INVALID_ARG;
+  }
+  if (!rope_dense_enough(so, B, T, H, d)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(y)) return FA_ERR_ALIGNMENT;
+  for (int i = 0; i < 3; ++i)
+    if ((st[i] & 7) || (so[i] & 7)) return FA_ERR_ALIGNMENT;
+  // in place (the same memory, the same strides) or apart
+  const bool same = x == y && st[0] == so[0] && st[1] == so[1] && st[2] == so[2];
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
+  const uintptr_t x1 = x0 + 2 * (uintptr_t)rope_extent(st, B, T, H, d);
+  const uintptr_t y1 = y0 + 2 * (uintptr_t)rope_extent(so, B, T, H, d);
+  if (!same && x0 < y1 && y0 < x1) return FA_ERR_INVALID_ARG;
+  r->x = reinterpret_cast<const __nv_bfloat16*>(x);
+  r->y = reinterpret_cast<__nv_bfloat16*>(y);
+  r->xb = st[0]; r->xt = st[1]; r->xh = st[2];
+  r->yb = so[0]; r->yt = so[1]; r->yh = so[2];
+  return FA_OK;
+}
+
+static int rope_impl(const void* q, void* q_out, const void* k, void* k_out, const int64_t* strides,
+                     const int* positions, const double* freqs, int rotary_dim, int interleaved, float amplitude,
+                     float sign, int B, int T, int Hq, int Hkv, int d, void* stream) {
+  if (B < 0 || T < 0 || Hq < 0 || Hkv < 0 || Hq + (int64_t)Hkv < 1 || Hq > 65535 || Hkv > 65535)
+    return FA_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (rotary_dim < 16 || rotary_dim > d || rotary_dim % 16 != 0 || !isfinite(amplitude)) return FA_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return FA_OK;
+  if (!strides || !freqs) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(freqs) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return FA_ERR_ALIGNMENT;
+  RopeParams p;
+  memset(&p, 0, sizeof(p));
+  int st = FA_OK;
+  if (Hq > 0) st = rope_tensor(&p.q, q, q_out, strides, strides + 3, B, T, Hq, d);
+  if (!st && Hkv > 0) st = rope_tensor(&p.k, k, k_out, strides + 6, strides + 9, B, T, Hkv, d);
+  if (st) return st;
+  p.positions = positions;
+  p.freqs = freqs;
+  p.n_tokens = (long long)B * T;
+  p.T = T;
+  p.Hq = Hq;
+  p.heads = Hq + Hkv;
+  p.rot = rotary_dim;
+  p.amplitude = amplitude;
+  p.sign = sign;
+  if ((st = device_setup())) return st;
+  const int tpb = p.n_tokens >= 4096 ? 4 : 1;
+  const long long blocks = (p.n_tokens + tpb - 1) / tpb;
+  if (blocks > 0x7FFFFFFFll) return FA_ERR_INVALID_ARG;
+  const size_t smem = (size_t)tpb * (rotary_dim / 2) * sizeof(float2);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d == 64 && interleaved)
+    fa_rope_kernel<64, true><<<(unsigned)blocks, 256, smem, s>>>(p, tpb);
+  else if (d == 64)
+    fa_rope_kernel<64, false><<<(unsigned)blocks, 256, smem, s>>>(p, tpb);
+  else if (interleaved)
+    fa_rope_kernel<128, true><<<(unsigned)blocks, 256, smem, s>>>(p, tpb);
+  else
+    fa_rope_kernel<128, false><<<(unsigned)blocks, 256, smem, s>>>(p, tpb);
+  return launch_status();
+}
+
+}  // namespace fa
+
+extern "C" int fa_rope(const void* q, void* q_out, const void* k, void* k_out, const int64_t* strides,
+                       const int* positions, const double* freqs, int rotary_dim, int interleaved, float amplitude,
+                       int B, int T, int Hq, int Hkv, int d, void* stream) {
+  return rope_impl(q, q_out, k, k_out, strides, positions, freqs, rotary_dim, interleaved, amplitude, 1.f, B, T, Hq,
+                   Hkv, d, stream);
+}
+
+extern "C" int fa_rope_backward(const void* dq, void* dq_out, const void* dk, void* dk_out, const int64_t* strides,
+                                const int* positions, const double* freqs, int rotary_dim, int interleaved,
+                                float amplitude, int B, int T, int Hq, int Hkv, int d, void* stream) {
+  return rope_impl(dq, dq_out, dk, dk_out, strides, positions, freqs, rotary_dim, interleaved, amplitude, -1.f, B, T,
+                   Hq, Hkv, d, stream);
+}
+
+// ---------------------------------------------------------------------------
+// The 4-bit cache
+// ---------------------------------------------------------------------------
+namespace fa {
+
+static int kv4_check_cache(const void* k_codes, const void* k_params, const void* v_codes, const void* v_params) {
+  for (const void* ptr : {k_codes, k_params, v_codes, v_params}) {
+    if (!ptr) return FA_ERR_INVALID_ARG;
+    if (!aligned16(ptr)) return FA_ERR_ALIGNMENT;
+  }
+  return FA_OK;
+}
+
+static int kv4_check_sizes(int B, int Hkv, int Tk_max, int d) {
+  if (B < 0 || Hkv < 1 || Tk_max < 0 || Tk_max % 64 != 0 || Tk_max > (1 << 30)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+static int kv4_rows_blocks(Kv4RowsParams* p, int B, int T, int Hkv, int Tk_max, int d, unsigned* blocks) {
+  p->T = T;
+  p->H = Hkv;
+  p->Tk_max = Tk_max;
+  const long long rows = (long long)B * T;
+  if (rows > (1ll << 40) / Hkv) return FA_ERR_INVALID_ARG;
+  p->units = rows * Hkv * (d / 8);
+  const long long n = (p->units + 255) / 256;
+  if (n > 0x7FFFFFFFll) return FA_ERR_INVALID_ARG;
+  *blocks = (unsigned)n;
+  return FA_OK;
+}
+
+}  // namespace fa
+
+extern "C" int fa_kv4_append(const void* k, const void* v, const int64_t* strides, void* k_codes, void* k_params,
+                             void* v_codes, void* v_params, const int* start, const int* count, int B, int T, int Hkv,
+                             int Tk_max, int d, void* stream) {
+  int st = kv4_check_sizes(B, Hkv, Tk_max, d);
+  if (st) return st;
+  if (T < 0) return FA_ERR_INVALID_ARG;
+  if (B == 0 || T == 0 || Tk_max == 0) return FA_OK;
+  if (!k || !v || !strides || !start) return FA_ERR_INVALID_ARG;
+  if ((st = kv4_check_cache(k_codes, k_params, v_codes, v_params))) return st;
+  for (int i = 0; i < 6; ++i)
+    if (strides[i] < 0 || strides[i] > (1ll << 40)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(start) & 3u) ||
+      (reinterpret_cast<uintptr_t>(count) & 3u))
+    return FA_ERR_ALIGNMENT;
+  for (int i = 0; i < 6; ++i)
+    if (strides[i] & 7) return FA_ERR_ALIGNMENT;
+  Kv4RowsParams p;
+  memset(&p, 0, sizeof(p));
+  unsigned blocks = 0;
+  if ((st = kv4_rows_blocks(&p, B, T, Hkv, Tk_max, d, &blocks))) return st;
+  p.x[0] = reinterpret_cast<const __nv_bfloat16*>(k);
+  p.x[1] = reinterpret_cast<const __nv_bfloat16*>(v);
+  for (int w = 0; w < 2; ++w) {
+    p.xb[w] = strides[3 * w];
+    p.xt[w] = strides[3 * w + 1];
+    p.xh[w] = strides[3 * w + 2];
+  }
+  p.codes[0] = reinterpret_cast<uint8_t*>(k_codes);
+  p.codes[1] = reinterpret_cast<uint8_t*>(v_codes);
+  p.params[0] = reinterpret_cast<__nv_bfloat16*>(k_params);
+  p.params[1] = reinterpret_cast<__nv_bfloat16*>(v_params);
+  p.start = start;
+  p.count = count;
+  if ((st = device_setup())) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d == 64)
+    fa_kv4_append_kernel<64><<<dim3(blocks, 2), 256, 0, s>>>(p);
+  else
+    fa_kv4_append_kernel<128><<<dim3(blocks, 2), 256, 0, s>>>(p);
+  return launch_status();
+}
+
+extern "C" int fa_kv4_read(void* k, void* v, const void* k_codes, const void* k_params, const void* v_codes,
+                           const void* v_params, const int* start, const int* count, int B, int T, int Hkv,
+                           int Tk_max, int d, void* stream) {
+  int st = kv4_check_sizes(B, Hkv, Tk_max, d);
+  if (st) return st;
+  if (T < 0) return FA_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return FA_OK;
+  if (!k || !v || !start) return FA_ERR_INVALID_ARG;
+  if (Tk_max > 0 && (st = kv4_check_cache(k_codes, k_params, v_codes, v_params))) return st;
+  if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(start) & 3u) ||
+      (reinterpret_cast<uintptr_t>(count) & 3u))
+    return FA_ERR_ALIGNMENT;
+  Kv4RowsParams p;
+  memset(&p, 0, sizeof(p));
+  unsigned blocks = 0;
+  if ((st = kv4_rows_blocks(&p, B, T, Hkv, Tk_max, d, &blocks))) return st;
+  p.y[0] = reinterpret_cast<__nv_bfloat16*>(k);
+  p.y[1] = reinterpret_cast<__nv_bfloat16*>(v);
+  p.codes[0] = reinterpret_cast<uint8_t*>(const_cast<void*>(k_codes));
+  p.codes[1] = reinterpret_cast<uint8_t*>(const_cast<void*>(v_codes));
+  p.params[0] = reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(k_params));
+  p.params[1] = reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(v_params));
+  p.start = start;
+  p.count = count;
+  if ((st = device_setup())) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d == 64)
+    fa_kv4_read_kernel<64><<<dim3(blocks, 2), 256, 0, s>>>(p);
+  else
+    fa_kv4_read_kernel<128><<<dim3(blocks, 2), 256, 0, s>>>(p);
+  return launch_status();
+}
+
+namespace fa {
+static constexpr int kKv4Chunk = 512;
+}  // namespace fa
+
+extern "C" size_t fa_kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int Tk_max, int d) {
+  if (B < 0 || Hq < 1 || Hkv < 1 || Tk_max < 0 || (d != 64 && d != 128)) return 0;
+  const size_t n = ((size_t)Tk_max + kKv4Chunk - 1) / kKv4Chunk;
+  return round256((size_t)B * Hq * n * d * 4) + round256((size_t)B * Hq * n * 8);
+}
+
+extern "C" int fa_kv4_decode(const void* q, const void* k_codes, const void* k_params, const void* v_codes,
+                             const void* v_params, const int* seqlens_k, void* o, float* lse, void* ws,
+                             size_t ws_bytes, int B, int Hq, int Hkv, int Tk_max, int d, float scale, int window,
+                             int sinks, void* stream) {
+  int st = kv4_check_sizes(B, Hkv, Tk_max, d);
+  if (st) return st;
+  if (Hq < 1 || Hq % Hkv != 0 || !isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (window < 0 || window > (1 << 30) || sinks < 0 || sinks > kMaxSinks || (sinks > 0 && window == 0))
+    return FA_ERR_INVALID_ARG;
+  const int G = Hq / Hkv;
+  if (G != 1 && G != 2 && G != 4 && G != 8) return FA_ERR_UNSUPPORTED;
+  if ((int64_t)B * Hq > (1 << 26) || (int64_t)B * Hkv > 65535) return FA_ERR_INVALID_ARG;
+  if (B == 0) return FA_OK;
+  if (!q || !seqlens_k || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (Tk_max > 0 && (st = kv4_check_cache(k_codes, k_params, v_codes, v_params))) return st;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(seqlens_k) & 3u))
+    return FA_ERR_ALIGNMENT;
+  if (!ws || ws_bytes < fa_kv4_decode_workspace_bytes(B, Hq, Hkv, Tk_max, d) || !aligned16(ws))
+    return FA_ERR_WORKSPACE;
+  if ((st = device_setup())) return st;
+  Kv4DecodeParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.k_codes = reinterpret_cast<const uint8_t*>(k_codes);
+  p.v_codes = reinterpret_cast<const uint8_t*>(v_codes);
+  p.k_params = reinterpret_cast<const __nv_bfloat16*>(k_params);
+  p.v_params = reinterpret_cast<const __nv_bfloat16*>(v_params);
+  p.seqlens = seqlens_k;
+  p.chunk = kKv4Chunk;
+  p.nsplit = (Tk_max + kKv4Chunk - 1) / kKv4Chunk;
+  p.ws_o = reinterpret_cast<float*>(ws);
+  p.ws_ml = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + round256((size_t)B * Hq * p.nsplit * d * 4));
+  p.o = reinterpret_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Tk_max = Tk_max;
+  p.window = window;
+  p.sinks = sinks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p.nsplit > 0) {
+    const dim3 grid((unsigned)p.nsplit, (unsigned)(B * Hkv));
+#define FA_KV4_LAUNCH(DD, GG) fa_kv4_split_kernel<DD, GG><<<grid, 128, 0, s>>>(p)
+    if (d == 64) {
+      if (G == 1) FA_KV4_LAUNCH(64, 1); else if (G == 2) FA_KV4_LAUNCH(64, 2);
+      else if (G == 4) FA_KV4_LAUNCH(64, 4); else FA_KV4_LAUNCH(64, 8);
+    } else {
+      if (G == 1) FA_KV4_LAUNCH(128, 1); else if (G == 2) FA_KV4_LAUNCH(128, 2);
+      else if (G == 4) FA_KV4_LAUNCH(128, 4); else FA_KV4_LAUNCH(128, 8);
+    }
+#undef FA_KV4_LAUNCH
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  }
+  const unsigned blocks = (unsigned)(((size_t)B * Hq * 32 + 255) / 256);
+  if (d == 64)
+    fa_kv4_combine_kernel<64><<<blocks, 256, 0, s>>>(p);
+  else
+    fa_kv4_combine_kernel<128><<<blocks, 256, 0, s>>>(p);
+  return launch_status();
 }

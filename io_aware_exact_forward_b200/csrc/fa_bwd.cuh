@@ -139,6 +139,14 @@ struct BwdParams {
   __nv_bfloat16* dv;
   int B, Hq, Hkv, Tq, Tk, causal;
   int window;          // > 0: sliding window of that many keys (implies causal)
+  // WIN == 2 (sinks): keys 0 .. sinks - 1 stay visible behind the window, so
+  // the key tiles that hold them, n_sink_tiles of them, see every later query
+  // tile.  Each is cut along its queries into `pieces` items, about as long as
+  // a windowed item; with more than one piece their dK and dV go to sink_part
+  // in fp32, [B * Hkv][n_sink_tiles][pieces][dV, dK][128][d], and are summed
+  // in order afterwards.
+  int sinks, n_sink_tiles, pieces;
+  float* sink_part;
   int Tq_pad;          // row pitch of lse2 / Dv
   float scale, scale_log2;
   int n_kv_tiles;
@@ -234,14 +242,33 @@ struct BwdCfg {
 // every query tile (of every query head of the GQA group) that sees it.
 struct BwdItem {
   int b, hkv, j0, qt_begin, nq, n_it;
+  int part;  // slot of sink_part that takes dK and dV, or -1: dk, dv themselves
 };
 
+template <int WIN>
 __device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int item) {
   BwdItem it;
+  it.part = -1;
   // Key tiles of one (batch, KV head) are adjacent in item order, so the
   // head's dQ accumulator rows and Q/dO tiles stay in L2 while they run.
-  const int kt = item % p.n_kv_tiles;
-  const int hb = item / p.n_kv_tiles;
+  int kt, hb, piece = 0;
+  if constexpr (WIN == 2) {
+    // the sink tiles' pieces first
+    const int n_part = p.B * p.Hkv * p.n_sink_tiles * p.pieces;
+    if (item < n_part) {
+      piece = item % p.pieces;
+      kt = item / p.pieces % p.n_sink_tiles;
+      hb = item / p.pieces / p.n_sink_tiles;
+      if (p.pieces > 1) it.part = item;
+    } else {
+      const int rest = p.n_kv_tiles - p.n_sink_tiles;
+      kt = p.n_sink_tiles + (item - n_part) % rest;
+      hb = (item - n_part) / rest;
+    }
+  } else {
+    kt = item % p.n_kv_tiles;
+    hb = item / p.n_kv_tiles;
+  }
   it.b = hb / p.Hkv;
   it.hkv = hb % p.Hkv;
   it.j0 = kt * 128;
@@ -255,6 +282,13 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdParams& p, int item) {
       // last query whose window still holds the tile's last key
       const long long qmax = (long long)it.j0 + 127 - (p.Tk - p.Tq) + p.window - 1;
       qt_end = qmax < 0 ? 0 : (int)min((long long)n_qt, qmax / 128 + 1);
+      if constexpr (WIN == 2) {
+        if (kt < p.n_sink_tiles) {
+          const int per = (n_qt - it.qt_begin + p.pieces - 1) / p.pieces;
+          it.qt_begin = min(n_qt, it.qt_begin + piece * per);
+          qt_end = min(n_qt, it.qt_begin + per);
+        }
+      }
     }
   }
   it.nq = max(0, qt_end - it.qt_begin);
@@ -297,8 +331,8 @@ __device__ __forceinline__ void dropout_keep_keyrow_64(uint32_t (&mask)[2], int 
   }
 }
 
-// WIN: sliding-window masking compiled in (a separate instantiation, so
-// that the plain path keeps its registers).  DQ = false: no dQ product,
+// WIN: sliding-window masking compiled in (1), with sinks behind the window
+// (2); separate instantiations, so that the plain path keeps its registers.  DQ = false: no dQ product,
 // read-out or reduce-adds (warps 16-19 idle); dQ then comes from the
 // separate, deterministic pass of fa_bwd_dq.cuh.  DROP: dropout on P, with the
 // keep mask of the forward regenerated per key row; the P^T warps write the
@@ -306,7 +340,7 @@ __device__ __forceinline__ void dropout_keep_keyrow_64(uint32_t (&mask)[2], int 
 // each per 16-query chunk, and the dS warps read the keep bits off the
 // dropped copy's zeros:
 //   dV += (P*Z)^T dO * s,   dS = P * (Z * s * dP - D),   s = 256 / t.
-template <int D, bool WIN, bool DROP = false, bool DQ = true>
+template <int D, int WIN, bool DROP = false, bool DQ = true>
 __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
   using C = BwdCfg<D, DROP, DQ>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -402,7 +436,7 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
       bool ok = true;
       int gi = 0, ki = 0, issued_kv = 0, n_do = 0;
       for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-        const BwdItem I = bwd_item(p, item);
+        const BwdItem I = bwd_item<WIN>(p, item);
         if (I.n_it == 0) continue;
         const int kvb = ki % C::NKV;
         if (ki >= C::NKV) ok = mbar_wait(bar_kv_empty(kvb), ((ki / C::NKV) - 1) & 1, wc);
@@ -464,7 +498,7 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
     bool ok = true;
     int gi = 0;
     for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-      const BwdItem I = bwd_item(p, item);
+      const BwdItem I = bwd_item<WIN>(p, item);
       const uint32_t cg = (uint32_t)(I.j0 >> 2) + (uint32_t)cl;
       for (int it = 0; it < I.n_it && ok; ++it, ++gi) {
         const int mb = gi & 1;
@@ -529,7 +563,7 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
       int gi = 0, ki = 0;
       bool started = false;
       for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-        const BwdItem I = bwd_item(p, item);
+        const BwdItem I = bwd_item<WIN>(p, item);
         if (I.n_it == 0) continue;
         const int kvb = ki % C::NKV;
         if (!started) {
@@ -661,7 +695,7 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
     bool ok = true;
     int gi = 0, ki = 0;
     for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-      const BwdItem I = bwd_item(p, item);
+      const BwdItem I = bwd_item<WIN>(p, item);
       const int key = I.j0 + j;
       const int qmin = key - (p.Tk - p.Tq);  // causal: first query that sees this key
       const bool key_ok = key < p.Tk;
@@ -692,7 +726,10 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
         const float* lrow = lse_s + s * 128 + 64 * half;
         const int cmin = p.causal ? qmin - q0 - 64 * half : 0;  // columns < cmin are masked
         // and, with a window, columns >= cmax (queries past this key's window)
-        const int cmax = WIN ? qmin + p.window - q0 - 64 * half : (1 << 30);
+        int cmax = WIN ? qmin + p.window - q0 - 64 * half : (1 << 30);
+        if constexpr (WIN == 2) {
+          if (key < p.sinks) cmax = 1 << 30;  // a sink stays visible
+        }
         const bool masked = __any_sync(0xffffffffu, !key_ok || cmin > 0 || (WIN && cmax < 64));
         // 64 query columns in four 16-column chunks; the load of chunk c+1
         // overlaps the exponentials of chunk c.  P^T (bf16 pairs) goes to
@@ -760,6 +797,17 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0u;
           }
+          if constexpr (WIN == 2) {
+            if (I.part >= 0) {
+              float4* d4 = reinterpret_cast<float4*>(
+                  p.sink_part + (((size_t)I.part * 2 + which) * 128 + j) * D + half * (D / 2) + c * 32);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                d4[i] = make_float4(__uint_as_float(v[4 * i]) * mul, __uint_as_float(v[4 * i + 1]) * mul,
+                                    __uint_as_float(v[4 * i + 2]) * mul, __uint_as_float(v[4 * i + 3]) * mul);
+              continue;
+            }
+          }
           uint4 pk[4];
           uint32_t* pw = reinterpret_cast<uint32_t*>(pk);
 #pragma unroll
@@ -788,7 +836,7 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
     bool ok = true;
     int gi = 0;
     for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-      const BwdItem I = bwd_item(p, item);
+      const BwdItem I = bwd_item<WIN>(p, item);
       for (int it = 0; it < I.n_it && ok; ++it, ++gi) {
         const int s = stg(gi), buf = gi % C::NSBUF;
         const uint32_t tP = tmem + C::TM_S0 + 128 * buf + lane_off + 64 * half;  // P^T (bf16 pairs)
@@ -899,7 +947,7 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
     bool ok = true;
     int gi = 0;
     for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-      const BwdItem I = bwd_item(p, item);
+      const BwdItem I = bwd_item<WIN>(p, item);
       for (int it = 0; it < I.n_it && ok; ++it, ++gi) {
         const int buf = gi % C::NSBUF;
         const int h = I.hkv * G + it / I.nq;
@@ -975,8 +1023,35 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
   }
 }
 
+// dK and dV of the sink tiles from their pieces, summed in the pieces' order.
+// One thread per four elements: grid (slots of 128 keys, [dV, dK]).
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_sink_sum_kernel(const float* __restrict__ part,
+                                                              __nv_bfloat16* __restrict__ dk,
+                                                              __nv_bfloat16* __restrict__ dv, int Hkv, int Tk,
+                                                              int n_sink_tiles, int pieces) {
+  const int kt = blockIdx.x % n_sink_tiles, hb = blockIdx.x / n_sink_tiles, which = blockIdx.y;
+  for (int i = threadIdx.x; i < 128 * D / 4; i += blockDim.x) {
+    const int j = i / (D / 4), c = i % (D / 4);
+    const int key = kt * 128 + j;
+    if (key >= Tk) continue;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int n = 0; n < pieces; ++n) {
+      const float4 x = *reinterpret_cast<const float4*>(
+          part + ((((size_t)blockIdx.x * pieces + n) * 2 + which) * 128 + j) * D + c * 4);
+      a.x += x.x;
+      a.y += x.y;
+      a.z += x.z;
+      a.w += x.w;
+    }
+    const size_t row = ((size_t)(hb / Hkv) * Tk + key) * Hkv + hb % Hkv;
+    *reinterpret_cast<uint2*>((which ? dk : dv) + row * D + c * 4) =
+        make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  }
+}
+
 static int bwd_setup() {
-  const void* kernels[10] = {reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<64, false>),
+  const void* kernels[14] = {reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<64, false>),
                             reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<64, true>),
                             reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<128, false>),
                             reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<128, true>),
@@ -985,8 +1060,12 @@ static int bwd_setup() {
                             reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<64, false, false, false>),
                             reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<64, true, false, false>),
                             reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<128, false, false, false>),
-                            reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<128, true, false, false>)};
-  const int bytes[10] = {BwdCfg<64>::SMEM_BYTES,
+                            reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<128, true, false, false>),
+                            reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<64, 2>),
+                            reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<128, 2>),
+                            reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<64, 2, false, false>),
+                            reinterpret_cast<const void*>(fa_bwd_dkdv_kernel<128, 2, false, false>)};
+  const int bytes[14] = {BwdCfg<64>::SMEM_BYTES,
                          BwdCfg<64>::SMEM_BYTES,
                          BwdCfg<128>::SMEM_BYTES,
                          BwdCfg<128>::SMEM_BYTES,
@@ -995,8 +1074,12 @@ static int bwd_setup() {
                          BwdCfg<64, false, false>::SMEM_BYTES,
                          BwdCfg<64, false, false>::SMEM_BYTES,
                          BwdCfg<128, false, false>::SMEM_BYTES,
+                         BwdCfg<128, false, false>::SMEM_BYTES,
+                         BwdCfg<64>::SMEM_BYTES,
+                         BwdCfg<128>::SMEM_BYTES,
+                         BwdCfg<64, false, false>::SMEM_BYTES,
                          BwdCfg<128, false, false>::SMEM_BYTES};
-  for (int i = 0; i < 10; ++i)
+  for (int i = 0; i < 14; ++i)
     if (cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes[i]) != cudaSuccess)
       return FA_ERR_CUDA;
   return FA_OK;

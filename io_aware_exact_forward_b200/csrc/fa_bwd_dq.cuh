@@ -40,6 +40,7 @@ struct DqParams {
   __nv_bfloat16* dq;   // bf16 [B][Tq][Hq][d], or null
   int B, Hq, Hkv, Tq, Tk, causal;
   int window;          // > 0: sliding window of that many keys (implies causal)
+  int sinks;           // WIN == 2: keys 0 .. sinks - 1 stay visible behind the window
   int Tq_pad;
   float scale, scale_log2;
   int n_qt;            // ceil(Tq / 128)
@@ -77,11 +78,20 @@ struct DqCfg {
 };
 
 // One work item: query tile [q0, q0 + 128) of head h of batch b against KV
-// tiles kt0 .. kt0 + n_kv - 1.
+// tiles kt0 .. kt0 + n_kv - 1; with sinks the first n_sink of the n_kv tiles
+// are tiles 0 .. n_sink - 1 and kt0 is the first tile after them.
 struct DqItem {
-  int b, h, hkv, q0, kt0, n_kv;
+  int b, h, hkv, q0, kt0, n_kv, n_sink;
 };
 
+// The KV tile that an item takes as its j-th.
+template <int WIN>
+__device__ __forceinline__ int dq_kv_tile(const DqItem& it, int j) {
+  if constexpr (WIN == 2) return j < it.n_sink ? j : it.kt0 + j - it.n_sink;
+  return it.kt0 + j;
+}
+
+template <int WIN>
 __device__ __forceinline__ DqItem dq_item(const DqParams& p, int item) {
   DqItem it;
   // The query tiles of one (batch, head) are adjacent in item order, so
@@ -106,11 +116,17 @@ __device__ __forceinline__ DqItem dq_item(const DqParams& p, int item) {
       it.kt0 = kmin <= 0 ? 0 : min(kt_end, kmin / 128);
     }
   }
-  it.n_kv = kt_end - it.kt0;
+  it.n_sink = 0;
+  if constexpr (WIN == 2) {
+    it.n_sink = min(kt_end, (p.sinks + 127) / 128);
+    it.kt0 = max(it.kt0, it.n_sink);
+  }
+  it.n_kv = kt_end - it.kt0 + it.n_sink;
   return it;
 }
 
-template <int D, bool WIN>
+// WIN: 0 no window, 1 a sliding window, 2 a window with sinks behind it.
+template <int D, int WIN>
 __global__ void __launch_bounds__(320, 1) fa_bwd_dq_kernel(const __grid_constant__ DqParams p) {
   using C = DqCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -137,7 +153,7 @@ __global__ void __launch_bounds__(320, 1) fa_bwd_dq_kernel(const __grid_constant
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   WaitCtl wc{abort_flag, p.wait_limit_ns};
-  const DqItem it = dq_item(p, blockIdx.x);
+  const DqItem it = dq_item<WIN>(p, blockIdx.x);
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -183,7 +199,7 @@ __global__ void __launch_bounds__(320, 1) fa_bwd_dq_kernel(const __grid_constant
         const int s = j % C::NST;
         if (j >= C::NST) ok = mbar_wait(bar_kv_empty(s), ((j / C::NST) - 1) & 1, wc);
         if (!ok) break;
-        const int k0 = (it.kt0 + j) * 128;
+        const int k0 = dq_kv_tile<WIN>(it, j) * 128;
         mbar_arrive_expect_tx(bar_kv_full(s), 2 * C::TILE);
         for (int kb = 0; kb < C::NBOX; ++kb) {
           tma_load_4d(aK(s) + kb * C::BOX_BYTES, &p.tm_k, bar_kv_full(s), kb * 64, it.hkv, k0, it.b);
@@ -277,9 +293,11 @@ __global__ void __launch_bounds__(320, 1) fa_bwd_dq_kernel(const __grid_constant
       // S_j and dP_j are in registers: the next tile's products may overwrite them
       tc_fence_before();
       mbar_arrive(bar_s_free);
-      const int kbase = (it.kt0 + j) * 128 + 64 * hc;
+      const int kbase = dq_kv_tile<WIN>(it, j) * 128 + 64 * hc;
       const int nvalid = key_limit - kbase;  // columns >= nvalid are masked
       const int nlo = key_lo - kbase;        // and columns < nlo
+      // columns below nsk are sinks: masked by the causal edge alone
+      const int nsk = WIN == 2 ? p.sinks - kbase : 0;
       const bool masked = __any_sync(0xffffffffu, nvalid < 64 || (WIN && nlo > 0));
       uint32_t ds[32];
 #pragma unroll
@@ -287,8 +305,8 @@ __global__ void __launch_bounds__(320, 1) fa_bwd_dq_kernel(const __grid_constant
         const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), sl2, nl2);
         float2 pr = make_float2(ex2_approx(x.x), ex2_approx(x.y));
         if (masked) {
-          if (2 * e >= nvalid || (WIN && 2 * e < nlo)) pr.x = 0.f;
-          if (2 * e + 1 >= nvalid || (WIN && 2 * e + 1 < nlo)) pr.y = 0.f;
+          if (2 * e >= nvalid || (WIN && 2 * e < nlo && (WIN != 2 || 2 * e >= nsk))) pr.x = 0.f;
+          if (2 * e + 1 >= nvalid || (WIN && 2 * e + 1 < nlo && (WIN != 2 || 2 * e + 1 >= nsk))) pr.y = 0.f;
         }
         const float2 t = __fadd2_rn(make_float2(__uint_as_float(dv[2 * e]), __uint_as_float(dv[2 * e + 1])), ndd);
         const float2 g = __fmul2_rn(pr, t);
@@ -355,13 +373,15 @@ __global__ void __launch_bounds__(320, 1) fa_bwd_dq_kernel(const __grid_constant
 }
 
 static int bwd_dq_setup() {
-  const void* kernels[4] = {reinterpret_cast<const void*>(fa_bwd_dq_kernel<64, false>),
+  const void* kernels[6] = {reinterpret_cast<const void*>(fa_bwd_dq_kernel<64, false>),
                             reinterpret_cast<const void*>(fa_bwd_dq_kernel<64, true>),
                             reinterpret_cast<const void*>(fa_bwd_dq_kernel<128, false>),
-                            reinterpret_cast<const void*>(fa_bwd_dq_kernel<128, true>)};
-  const int bytes[4] = {DqCfg<64>::SMEM_BYTES, DqCfg<64>::SMEM_BYTES, DqCfg<128>::SMEM_BYTES,
-                        DqCfg<128>::SMEM_BYTES};
-  for (int i = 0; i < 4; ++i)
+                            reinterpret_cast<const void*>(fa_bwd_dq_kernel<128, true>),
+                            reinterpret_cast<const void*>(fa_bwd_dq_kernel<64, 2>),
+                            reinterpret_cast<const void*>(fa_bwd_dq_kernel<128, 2>)};
+  const int bytes[6] = {DqCfg<64>::SMEM_BYTES, DqCfg<64>::SMEM_BYTES, DqCfg<128>::SMEM_BYTES,
+                        DqCfg<128>::SMEM_BYTES, DqCfg<64>::SMEM_BYTES, DqCfg<128>::SMEM_BYTES};
+  for (int i = 0; i < 6; ++i)
     if (cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes[i]) != cudaSuccess)
       return FA_ERR_CUDA;
   return FA_OK;

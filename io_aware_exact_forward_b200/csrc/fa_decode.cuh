@@ -45,6 +45,7 @@ struct DecodeParams {
   int B, Hq, Hkv, Tk_max, chunk, nchunk;
   int n_items;               // B * Hkv * nchunk (items past a sequence's end are skipped)
   int window;                // > 0: the query sees only the last `window` keys of its sequence
+  int sinks;                 // SINK instantiation: and its first `sinks` keys
   float scale_log2;
   unsigned long long wait_limit_ns;
 };
@@ -105,8 +106,31 @@ __device__ __forceinline__ uint32_t swz_off(int key, int ch) {
 // split kernel wrote.
 __device__ __forceinline__ int clamp_seqlen(const DecodeParams& p, int n) { return min(max(n, 0), p.Tk_max); }
 
-// Item k covers chunk k % nchunk of (sequence, KV head) k / nchunk.
-template <int D, int G>
+// Chunks of a sequence that hold a visible key when sinks stay visible behind
+// the window: chunks 0 .. n_sink - 1, then lo .. end - 1, `count` in all.
+struct SinkChunks {
+  int n_sink, lo, count;
+  __device__ __forceinline__ SinkChunks(const DecodeParams& p, int seqlen) {
+    const int end = (seqlen + p.chunk - 1) / p.chunk;
+    n_sink = min(end, (p.sinks + p.chunk - 1) / p.chunk);
+    lo = max(n_sink, max(0, seqlen - p.window) / p.chunk);
+    count = n_sink + max(0, end - lo);
+  }
+  __device__ __forceinline__ int at(int v) const { return v < n_sink ? v : lo + v - n_sink; }
+};
+
+// Keys of the chunk at k0 up to its last visible one: all that the sequence
+// has there, or, in a chunk wholly before the window, its sinks.
+template <bool SINK>
+__device__ __forceinline__ int chunk_keys(const DecodeParams& p, int k0, int seqlen) {
+  const int n = min(p.chunk, seqlen - k0);
+  if (SINK && k0 + n <= seqlen - p.window) return min(n, p.sinks - k0);
+  return n;
+}
+
+// Item k covers chunk k % nchunk of (sequence, KV head) k / nchunk; with SINK
+// the (k % nchunk)-th visible chunk, nchunk being the most that a sequence has.
+template <int D, int G, bool SINK = false>
 __global__ void __launch_bounds__(DecCfg<D, G>::THREADS)
 fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
   using C = DecCfg<D, G>;
@@ -153,13 +177,18 @@ fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
       bool ok = true;
       int t = 0, qi = 0;  // ring slot counter and item counter, continuous across items
       for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-        const int c = item % p.nchunk;
+        int c = item % p.nchunk;
         const int bh = item / p.nchunk;
         const int b = bh / p.Hkv, hkv = bh % p.Hkv;
-        const int k0 = c * p.chunk;
         const int seqlen = seqlen_of(b);
-        if (k0 >= seqlen || (p.window > 0 && k0 + p.chunk <= seqlen - p.window)) continue;
-        const int nsub = (min(p.chunk, seqlen - k0) + C::SUB - 1) / C::SUB;
+        if constexpr (SINK) {
+          const SinkChunks sc(p, seqlen);
+          if (c >= sc.count) continue;
+          c = sc.at(c);
+        }
+        const int k0 = c * p.chunk;
+        if (!SINK && (k0 >= seqlen || (p.window > 0 && k0 + p.chunk <= seqlen - p.window))) continue;
+        const int nsub = (chunk_keys<SINK>(p, k0, seqlen) + C::SUB - 1) / C::SUB;
         // the G query rows of the group are contiguous: one bulk copy
         const int qs = qi & 1;
         if (qi >= 2) ok = mbar_wait(bar_qempty(qs), ((qi >> 1) - 1) & 1, wc);
@@ -199,13 +228,20 @@ fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
   bool ok = true;
   int t = 0, qi = 0;
   for (int item = blockIdx.x; item < p.n_items; item += gridDim.x) {
-    const int c = item % p.nchunk;
+    const int v_idx = item % p.nchunk;  // slot of this chunk's partial result
+    int c = v_idx;
     const int bh = item / p.nchunk;
     const int b = bh / p.Hkv, hkv = bh % p.Hkv;
-    const int k0 = c * p.chunk;
     const int seqlen = seqlen_of(b);
-    if (k0 >= seqlen || (p.window > 0 && k0 + p.chunk <= seqlen - p.window)) continue;
-    const int nkeys = min(p.chunk, seqlen - k0);
+    if constexpr (SINK) {
+      const SinkChunks sc(p, seqlen);
+      if (c >= sc.count) continue;
+      c = sc.at(c);
+    }
+    const int k0 = c * p.chunk;
+    if (!SINK && (k0 >= seqlen || (p.window > 0 && k0 + p.chunk <= seqlen - p.window))) continue;
+    const int nkeys = chunk_keys<SINK>(p, k0, seqlen);
+    const int nsk = SINK ? p.sinks - k0 : 0;  // keys of the chunk below this bound are sinks
     // keys of the chunk before this bound are outside the window
     const int klo = p.window > 0 ? seqlen - p.window - k0 : -(1 << 30);
     const int nsub = (nkeys + C::SUB - 1) / C::SUB;
@@ -263,7 +299,8 @@ fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
       const int kk[4] = {kb0, kb0 + 1, kb0 + 8, kb0 + 9};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        sc[e] = (kk[e] < nkeys && kk[e] >= klo && real_row) ? sc[e] * p.scale_log2 : -INFINITY;
+        sc[e] = (kk[e] < nkeys && (kk[e] >= klo || (SINK && kk[e] < nsk)) && real_row) ? sc[e] * p.scale_log2
+                                                                                     : -INFINITY;
       float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -299,6 +336,21 @@ fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
         // (keys +0..7, d 8nb+8..), (keys +8..15, d 8nb+8..)
         const int vrow = kw + ((lane >> 3) & 1) * 8 + (lane & 7);
         const int vcol = lane >> 4;
+        if constexpr (SINK) {
+          // A masked key's P is 0, but 0 times what an unwritten cache row
+          // may hold (NaN, infinity) is not: such rows are zeroed first.
+          const int r0 = i * C::SUB + kw;
+          if (r0 + 16 > nkeys || (r0 < klo && r0 + 16 > nsk)) {
+            for (int idx = lane; idx < 16 * (D / 8); idx += 32) {
+              const int r = idx / (D / 8);
+              if (r0 + r >= nkeys || (r0 + r < klo && r0 + r >= nsk))
+                *reinterpret_cast<uint4*>(smem + C::OFF_RING + sV * C::STAGE_BYTES + swz_off(kw + r, idx % (D / 8))) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();  // before the next bulk load into this stage
+            __syncwarp();
+          }
+        }
 #pragma unroll
         for (int nb = 0; nb < D / 8; nb += 2) {
           uint32_t b0, b1, b2, b3;
@@ -339,8 +391,8 @@ fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
         O = fmaf(f, mrg[(w * G + gg) * D + dd], O);
       }
       const size_t row = (size_t)b * p.Hq + hkv * G + gg;
-      p.ws_o[(row * p.nchunk + c) * D + dd] = O / L;
-      if (dd == 0) p.ws_lse[row * p.nchunk + c] = (M + log2f(L)) * 0.69314718055994531f;
+      p.ws_o[(row * p.nchunk + v_idx) * D + dd] = O / L;
+      if (dd == 0) p.ws_lse[row * p.nchunk + v_idx] = (M + log2f(L)) * 0.69314718055994531f;
     }
     // The merge scratch is reused by the next item only after this barrier.
     // After an expired wait every compute warp has still passed the same
@@ -369,18 +421,27 @@ __device__ __forceinline__ void store_row(const DecodeParams& p, int row, int la
 }
 
 // Separate merge of the chunk partials: one warp per (sequence, query head).
-template <int D>
+// SINK: the partials are those of the visible chunks, in order, and rows of
+// sequences without keys are written here too.
+template <int D, bool SINK = false>
 __global__ void __launch_bounds__(256) fa_decode_combine_kernel(const __grid_constant__ DecodeParams p) {
   const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (gw >= p.B * p.Hq) return;
   const int b = gw / p.Hq;
   const int seqlen = clamp_seqlen(p, p.seqlens[b]);
-  const int nch = (seqlen + p.chunk - 1) / p.chunk;
-  if (nch == 0) return;  // written by fa_decode_empty_kernel
-  // with a window the chunks before the first visible key were skipped
-  const int c_lo = p.window > 0 ? max(0, seqlen - p.window) / p.chunk : 0;
   constexpr int E = D / 32;
+  const int nch = SINK ? SinkChunks(p, seqlen).count : (seqlen + p.chunk - 1) / p.chunk;
+  if (nch == 0) {
+    if constexpr (SINK) {
+      const float zero[E] = {};
+      store_row<D>(p, gw, lane, zero);
+      if (lane == 0) p.lse[gw] = -INFINITY;
+    }
+    return;  // without sinks written by fa_decode_empty_kernel
+  }
+  // with a window the chunks before the first visible key were skipped
+  const int c_lo = !SINK && p.window > 0 ? max(0, seqlen - p.window) / p.chunk : 0;
   const float* lse_c = p.ws_lse + (size_t)gw * p.nchunk;
   const float* o_c = p.ws_o + (size_t)gw * p.nchunk * D;
   float mx = -INFINITY;

@@ -80,6 +80,7 @@ struct FwdParams {
   int B, Hq, Hkv, Tq, Tk;
   int causal;
   int window;         // > 0: sliding window of that many keys (implies causal)
+  int sinks;          // SINK instantiation: keys 0 .. sinks - 1 stay visible behind the window
   float scale_log2;   // scale * log2(e) (times the q and k factors for E4M3 inputs)
   float o_scale;      // multiplies O = u / l: 1, the v factor for E4M3 inputs, or 256 / t with dropout
   uint32_t drop_t;    // dropout: keep iff the Philox byte < drop_t (1..255)
@@ -157,12 +158,20 @@ struct FwdCfg {
 };
 
 // One work item: two query tiles [m0, m0 + 256) of head h of batch b,
-// against KV tiles kv0 .. kv0 + n_kv - 1.
+// against KV tiles kv0 .. kv0 + n_kv - 1; with sinks the first n_sink of the
+// n_kv tiles are tiles 0 .. n_sink - 1 and kv0 is the first tile after them.
 struct FwdItem {
-  int b, h, hkv, m0, kv0, n_kv;
+  int b, h, hkv, m0, kv0, n_kv, n_sink;
 };
 
-template <int D>
+// The KV tile that an item takes as its j-th.
+template <bool SINK>
+__device__ __forceinline__ int fwd_kv_tile(const FwdItem& it, int j) {
+  if constexpr (SINK) return j < it.n_sink ? j : it.kv0 + j - it.n_sink;
+  return it.kv0 + j;
+}
+
+template <int D, bool SINK>
 __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int item) {
   using C = FwdCfg<D>;  // BM and BN are the same for both element types
   FwdItem it;
@@ -177,6 +186,7 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int item) {
   const int n_kv_all = (p.Tk + C::BN - 1) / C::BN;
   it.kv0 = 0;
   it.n_kv = n_kv_all;
+  it.n_sink = 0;
   if (p.causal) {
     const int last_row = min(it.m0 + 2 * C::BM, p.Tq) - 1;
     const int kmax = last_row + (p.Tk - p.Tq);  // last visible key (inclusive)
@@ -186,13 +196,22 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int item) {
       // before it are skipped
       const int kmin = it.m0 + (p.Tk - p.Tq) - p.window + 1;
       it.kv0 = kmin <= 0 ? 0 : min(it.n_kv, kmin / C::BN);
-      it.n_kv -= it.kv0;
+      if constexpr (SINK) {
+        // tiles that hold sinks come first, each tile once
+        it.n_sink = min(it.n_kv, (p.sinks + C::BN - 1) / C::BN);
+        it.kv0 = max(it.kv0, it.n_sink);
+        it.n_kv -= it.kv0 - it.n_sink;
+      } else {
+        it.n_kv -= it.kv0;
+      }
     }
   }
   return it;
 }
 
-template <int D, bool F8 = false, bool DROP = false>
+// SINK: a sliding window with the first keys visible behind it (a separate
+// instantiation, so that the plain path keeps its registers).
+template <int D, bool F8 = false, bool DROP = false, bool SINK = false>
 __global__ void __launch_bounds__(FwdCfg<D, F8, DROP>::THREADS, 1) fa_fwd_kernel(const __grid_constant__ FwdParams p) {
   using C = FwdCfg<D, F8, DROP>;
   extern __shared__ uint8_t smem_raw[];
@@ -267,7 +286,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, DROP>::THREADS, 1) fa_fwd_kernel
       int qi = 0;         // items with work, in this CTA's order
       int idx = 0;        // K/V ring slot counter
       for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-        const FwdItem it = fwd_item<D>(p, item);
+        const FwdItem it = fwd_item<D, SINK>(p, item);
         if (it.n_kv == 0) continue;
         const int qb = qi & 1;
         if (qi >= 2) ok = mbar_wait(bar_q_empty(qb), ((qi >> 1) - 1) & 1, wc);
@@ -288,9 +307,9 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, DROP>::THREADS, 1) fa_fwd_kernel
             mbar_arrive_expect_tx(bar_kv_full(pi), 2 * C::TILE_BYTES);
             for (int kb = 0; kb < C::NBOX; ++kb) {
               tma_load_4d(stage_addr(2 * pi) + kb * C::BOX_BYTES, &p.tm_k, bar_kv_full(pi), kb * 64, it.hkv,
-                          (it.kv0 + j) * C::BN, it.b);
+                          fwd_kv_tile<SINK>(it, j) * C::BN, it.b);
               tma_load_4d(stage_addr(2 * pi + 1) + kb * C::BOX_BYTES, &p.tm_v, bar_kv_full(pi), kb * 64, it.hkv,
-                          (it.kv0 + j) * C::BN, it.b);
+                          fwd_kv_tile<SINK>(it, j) * C::BN, it.b);
             }
             idx += 2;
           } else {
@@ -303,7 +322,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, DROP>::THREADS, 1) fa_fwd_kernel
               const CUtensorMap* tm = which ? &p.tm_v : &p.tm_k;
               for (int kb = 0; kb < C::NBOX; ++kb)
                 tma_load_4d(stage_addr(s) + kb * C::BOX_BYTES, tm, bar_kv_full(s), kb * C::BOX_ELEMS, it.hkv,
-                            (it.kv0 + j) * C::BN, it.b);
+                            fwd_kv_tile<SINK>(it, j) * C::BN, it.b);
             }
           }
         }
@@ -336,7 +355,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, DROP>::THREADS, 1) fa_fwd_kernel
     bool ok = true;
     int g = 0;
     for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-      const FwdItem it = fwd_item<D>(p, item);
+      const FwdItem it = fwd_item<D, SINK>(p, item);
       if (it.n_kv == 0) continue;
       const uint32_t a_glob = (uint32_t)((it.m0 + wq * C::BM) >> 2) + (uint32_t)a_loc;
       const uint32_t bh = (uint32_t)(it.b * p.Hq + it.h);
@@ -344,7 +363,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, DROP>::THREADS, 1) fa_fwd_kernel
         const int t = g + j, buf = t & 1;
         if (t >= 2) ok = mbar_wait(bar_mask_empty(buf), ((t >> 1) - 1) & 1, wc);
         if (!ok) break;
-        const uint32_t c0 = (uint32_t)((it.kv0 + j) * C::BN) >> 2;
+        const uint32_t c0 = (uint32_t)(fwd_kv_tile<SINK>(it, j) * C::BN) >> 2;
         uint32_t* mw = reinterpret_cast<uint32_t*>(mbuf + (buf * 2 + wq) * 128 + 4 * a_loc);
 #pragma unroll
         for (int k = 2 * kh; k < 2 * kh + 2; ++k) {  // keys 32k .. 32k + 31: eight Philox blocks
@@ -420,7 +439,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, DROP>::THREADS, 1) fa_fwd_kernel
           }
         };
         for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-          const FwdItem it = fwd_item<D>(p, item);
+          const FwdItem it = fwd_item<D, SINK>(p, item);
           if (it.n_kv == 0) continue;
           const int qb = qi & 1;
           ok = mbar_wait(bar_q_full(qb), (qi >> 1) & 1, wc);
@@ -465,7 +484,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, DROP>::THREADS, 1) fa_fwd_kernel
         }
       } else {
         for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-          const FwdItem it = fwd_item<D>(p, item);
+          const FwdItem it = fwd_item<D, SINK>(p, item);
           if (it.n_kv == 0) continue;
           const int qb = qi & 1;
           ok = mbar_wait(bar_q_full(qb), (qi >> 1) & 1, wc);
@@ -529,7 +548,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, DROP>::THREADS, 1) fa_fwd_kernel
     bool ok = true;
     int qi = 0, g = 0;
     for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-      const FwdItem it = fwd_item<D>(p, item);
+      const FwdItem it = fwd_item<D, SINK>(p, item);
       const int row = it.m0 + w * C::BM + r;
       const int key_limit = p.causal ? min(p.Tk, row + (p.Tk - p.Tq) + 1) : p.Tk;  // keys < limit visible
       const int key_lo = p.window > 0 ? row + (p.Tk - p.Tq) - p.window + 1 : 0;     // and keys >= key_lo
@@ -551,7 +570,7 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, DROP>::THREADS, 1) fa_fwd_kernel
           keep[3] = kv.w;
           mbar_arrive(bar_mask_empty(mb));
         } else if constexpr (DROP) {
-          dropout_keep_128(keep, row, (it.kv0 + j) * C::BN, (uint32_t)(it.b * p.Hq + it.h), p.drop_offset,
+          dropout_keep_128(keep, row, fwd_kv_tile<SINK>(it, j) * C::BN, (uint32_t)(it.b * p.Hq + it.h), p.drop_offset,
                            p.seed_lo, p.seed_hi, p.drop_t);
         }
         ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full(w), (g + j) & 1, wc));
@@ -566,13 +585,15 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, DROP>::THREADS, 1) fa_fwd_kernel
           tc_fence_before();
           mbar_arrive(bar_s_free(w));
         }
-        const int nvalid = key_limit - (it.kv0 + j) * C::BN;  // columns >= nvalid are masked
-        const int nlo = key_lo - (it.kv0 + j) * C::BN;         // and columns < nlo
+        const int nvalid = key_limit - fwd_kv_tile<SINK>(it, j) * C::BN;  // columns >= nvalid are masked
+        const int nlo = key_lo - fwd_kv_tile<SINK>(it, j) * C::BN;         // and columns < nlo
         const bool masked = __any_sync(0xffffffffu, nvalid < C::BN || nlo > 0);
         if (masked) {
+          // columns below nsk are sinks: masked by the causal edge alone
+          const int nsk = SINK ? p.sinks - fwd_kv_tile<SINK>(it, j) * C::BN : 0;
 #pragma unroll
           for (int c = 0; c < 128; ++c)
-            if (c >= nvalid || c < nlo) su[c] = __float_as_uint(-INFINITY);
+            if (c >= nvalid || (c < nlo && (!SINK || c >= nsk))) su[c] = __float_as_uint(-INFINITY);
         }
         // Row maximum: eight independent chains of three-input maxima (two
         // new columns per step), then a short tree.

@@ -1,0 +1,197 @@
+"""Host-side checks of the rotary, sink and 4-bit-cache entry points: bad calls
+are refused before anything is launched (no GPU needed)."""
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+import io_aware_exact_forward_b200 as fa
+
+N = None
+INVALID, UNSUPPORTED, ALIGN, WS = 1, 2, 3, 4
+
+
+@pytest.fixture
+def mem():
+    buf = (ctypes.c_uint8 * 8192)()
+    base = ctypes.addressof(buf) + (-ctypes.addressof(buf)) % 256
+    yield lambda off=0: ctypes.c_void_p(base + off)
+    del buf
+
+
+def strides(*v):
+    return (ctypes.c_longlong * len(v))(*v)
+
+
+def test_sink_entry_points():
+    lib = fa.load_library()
+    f = lambda w, s, d=64, Tq=16: lib.fa_forward_sinks(N, N, N, N, N, 1, 1, 1, Tq, 16, d, 1.0, w, s, N)  # noqa: E731
+    assert f(0, 4) == INVALID and f(-1, 4) == INVALID
+    assert f(4, -1) == INVALID and f(4, 1025) == INVALID
+    assert f(4, 4, d=96) == UNSUPPORTED
+    assert f(4, 4) == INVALID            # null pointers
+    assert f(4, 4, Tq=0) == 0
+    b = lambda w, s, det=0, d=64, B=1: lib.fa_backward_sinks(  # noqa: E731
+        *([N] * 9), N, 0, B, 1, 1, 16, 16, d, 1.0, w, s, det, N)
+    assert b(0, 4) == INVALID and b(4, -1) == INVALID and b(4, 1025) == INVALID and b(4, 4, det=2) == INVALID
+    assert b(4, 4, d=80) == UNSUPPORTED
+    assert b(4, 4) == INVALID
+    assert b(4, 4, B=0) == 0
+    c = lambda w, s: lib.fa_decode_splitkv_sinks(*([N] * 6), N, 0, 2, 32, 8, 1024, 128, 0.1, 256, w, s, N)  # noqa: E731
+    assert c(0, 4) == INVALID and c(8, -2) == INVALID and c(8, 1025) == INVALID and c(8, 4) == INVALID
+    assert lib.fa_decode_splitkv_sinks(*([N] * 6), N, 0, 2, 32, 2, 1024, 128, 0.1, 256, 8, 4, N) == UNSUPPORTED
+
+
+def test_sink_backward_workspace(mem):
+    lib = fa.load_library()
+    base = lib.fa_backward_workspace_bytes(1, 4, 2, 4096, 4096, 64)
+    more = lib.fa_backward_sinks_workspace_bytes(1, 4, 2, 4096, 4096, 64, 256, 4)
+    # 32 query tiles in pieces of max(4, 256 / 128 + 1) = 4: 8 pieces of one 128-key tile and 2 KV heads
+    assert more - base == 2 * 8 * 2 * 128 * 64 * 4
+    assert lib.fa_backward_sinks_workspace_bytes(1, 4, 2, 256, 256, 64, 256, 4) == \
+        lib.fa_backward_workspace_bytes(1, 4, 2, 256, 256, 64)
+    # a workspace that only the plain backward could do with
+    args = [mem()] * 9
+    assert lib.fa_backward_sinks(*args, mem(), base, 1, 4, 2, 4096, 4096, 64, 1.0, 256, 4, 0, N) == WS
+    assert lib.fa_backward_sinks(*args, N, more, 1, 4, 2, 4096, 4096, 64, 1.0, 256, 4, 0, N) == WS
+
+
+def test_sinks_need_a_window():
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="window"):
+        fa.forward(q, q, q, sinks=4)
+    with pytest.raises(ValueError, match="window"):
+        fa.backward(q, q, q, q, q, q, sinks=4)
+    with pytest.raises(ValueError, match="window"):
+        fa.decode_splitkv(q[0], q, q, q, sinks=4)
+    with pytest.raises(ValueError, match="window"):
+        fa.kv4_decode(q[0], None, None, sinks=4)
+
+
+def test_rope_arguments(mem):
+    lib = fa.load_library()
+    T, H, d = 2, 2, 64
+    dense = (T * H * d, H * d, d)
+    st = strides(*dense * 4)
+
+    def call(q=0, q_out=1024, k=2048, k_out=3072, st=st, freqs=4096, rot=64, inter=0, amp=1.0, B=1, T=T, Hq=H,
+             Hkv=H, d=d, pos=N):
+        p = lambda x: N if x is None else mem(x)  # noqa: E731
+        return lib.fa_rope(p(q), p(q_out), p(k), p(k_out), st, pos, p(freqs), rot, inter, amp, B, T, Hq, Hkv, d, N)
+
+    assert call(d=96) == UNSUPPORTED
+    for rot in (0, 8, 24, 80, -16):
+        assert call(rot=rot) == INVALID, rot
+    assert call(inter=2) == INVALID
+    assert call(amp=math.nan) == INVALID
+    assert call(Hq=0, Hkv=0) == INVALID
+    assert call(B=-1) == INVALID
+    assert call(B=0) == 0 and call(T=0) == 0
+    assert call(freqs=None) == INVALID and call(q=None) == INVALID and call(k_out=None) == INVALID
+    assert call(st=N) == INVALID
+    assert call(q=8) == ALIGN and call(freqs=4100) == ALIGN
+    assert call(pos=mem(4098)) == ALIGN
+    # the output overlaps its input without being it
+    assert call(q_out=256) == INVALID
+    # token strides: not a multiple of 8, negative, and outputs whose elements share places
+    assert call(st=strides(*dense, *dense, *dense, T * H * d, H * d + 4, d)) == ALIGN
+    assert call(st=strides(-8, H * d, d, *dense * 3)) == INVALID
+    assert call(st=strides(*dense, 0, 0, d, *dense * 2)) == INVALID
+    assert call(st=strides(*dense, T * H * d, d, d, *dense * 2)) == INVALID
+    for f in (lib.fa_rope_backward,):
+        assert f(N, N, N, N, st, N, mem(0), 64, 0, 1.0, 1, T, H, H, 96, N) == UNSUPPORTED
+
+
+def test_kv4_arguments(mem):
+    lib = fa.load_library()
+    st = strides(*(2 * 64, 2 * 64, 64) * 2)
+
+    def append(k=0, v=512, codes=1024, start=2048, count=N, B=1, T=1, Hkv=2, Tk=64, d=64, st=st):
+        p = lambda x: N if x is None else mem(x)  # noqa: E731
+        return lib.fa_kv4_append(p(k), p(v), st, *([p(codes)] * 4), p(start), count, B, T, Hkv, Tk, d, N)
+
+    assert append(d=96) == UNSUPPORTED
+    assert append(Tk=65) == INVALID and append(Tk=-64) == INVALID and append(T=-1) == INVALID
+    assert append(Hkv=0) == INVALID
+    assert append(B=0) == 0 and append(T=0) == 0 and append(Tk=0) == 0
+    assert append(k=None) == INVALID and append(codes=None) == INVALID and append(start=None) == INVALID
+    assert append(k=8) == ALIGN and append(codes=1032) == ALIGN and append(start=2049) == ALIGN
+    assert append(st=strides(128, 128, 60, 128, 128, 64)) == ALIGN
+    assert append(st=strides(-128, 128, 64, 128, 128, 64)) == INVALID
+
+    def read(k=0, codes=1024, start=2048, Tk=64, d=64, T=1):
+        p = lambda x: N if x is None else mem(x)  # noqa: E731
+        return lib.fa_kv4_read(p(k), p(k), *([p(codes)] * 4), p(start), N, 1, T, 2, Tk, d, N)
+
+    assert read(d=32) == UNSUPPORTED and read(Tk=100) == INVALID and read(T=-2) == INVALID and read(T=0) == 0
+    assert read(k=None) == INVALID and read(codes=None) == INVALID and read(start=None) == INVALID
+    assert read(k=4) == ALIGN
+
+    def decode(q=0, codes=1024, lens=2048, ws=4096, wsb=1 << 20, B=1, Hq=4, Hkv=2, Tk=64, d=64, scale=1.0, window=0,
+               sinks=0):
+        p = lambda x: N if x is None else mem(x)  # noqa: E731
+        return lib.fa_kv4_decode(p(q), *([p(codes)] * 4), p(lens), p(0), p(0), p(ws), wsb, B, Hq, Hkv, Tk, d, scale,
+                                 window, sinks, N)
+
+    assert decode(d=96) == UNSUPPORTED and decode(Hq=6) == UNSUPPORTED and decode(Hq=32) == UNSUPPORTED
+    assert decode(Hq=3) == INVALID and decode(Tk=96) == INVALID and decode(scale=math.inf) == INVALID
+    assert decode(window=-1) == INVALID and decode(sinks=4) == INVALID and decode(window=4, sinks=1025) == INVALID
+    assert decode(B=0) == 0
+    assert decode(q=None) == INVALID and decode(lens=None) == INVALID and decode(codes=None) == INVALID
+    assert decode(q=4) == ALIGN
+    assert decode(ws=None) == WS and decode(wsb=16) == WS and decode(ws=4100) == WS
+    assert lib.fa_kv4_decode_workspace_bytes(1, 4, 2, 64, 96) == 0
+
+
+def test_bindings_refuse():
+    x = torch.zeros(1, 2, 2, 64, dtype=torch.bfloat16)
+    f = torch.zeros(32, dtype=torch.float64)
+    with pytest.raises(ValueError, match="CUDA"):
+        fa.rope(x, x, f)
+    with pytest.raises(ValueError, match="q must be"):
+        fa.rope(x[0], x[0], f)
+    with pytest.raises(ValueError):
+        fa.kv4_cache(1, 2, 100, 96, device="cpu")
+    c = fa.kv4_cache(1, 2, 100, 64, device="cpu")
+    assert c.k_codes.shape == (1, 2, 128, 32) and c.v_params.shape == (1, 2, 128, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        fa.kv4_append(x, x, c, torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="CUDA"):
+        fa.kv4_read(c, torch.zeros(1, dtype=torch.int32), 2)
+    with pytest.raises(ValueError, match="window"):
+        fa.kv4_decode(x[0], c, torch.zeros(1, dtype=torch.int32), window=0)
+
+
+def test_rope_frequencies():
+    """Against the definitions, pair by pair."""
+    f, a = fa.rope_frequencies(64, 10000.0)
+    assert a == 1.0 and f.dtype == torch.float64
+    want = [10000.0 ** (-2 * i / 64) for i in range(32)]
+    assert max(abs(float(f[i]) / want[i] - 1) for i in range(32)) < 1e-14
+    f4, _ = fa.rope_frequencies(64, 10000.0, "linear", 4.0)
+    assert torch.allclose(f4 * 4, f, rtol=1e-14, atol=0)
+    # ntk: the fastest pair stays, the slowest is stretched by the factor
+    fn, _ = fa.rope_frequencies(64, 10000.0, "ntk", 4.0)
+    assert float(fn[0]) == 1.0 and abs(float(f[-1] / fn[-1]) - 4.0) < 1e-12
+    # within the trained length nothing changes; beyond it the factor follows the length
+    same, _ = fa.rope_frequencies(64, 10000.0, "ntk", 2.0, trained_length=4096, length=4096)
+    assert torch.allclose(same, f, rtol=1e-14, atol=0)
+    longer, _ = fa.rope_frequencies(64, 10000.0, "ntk", 2.0, trained_length=4096, length=8192)
+    assert abs(float(f[-1] / longer[-1]) - 3.0) < 1e-12
+    # yarn: many turns kept, few turns interpolated, monotone between; amplitude from the factor
+    fy, ay = fa.rope_frequencies(128, 10000.0, "yarn", 8.0, trained_length=4096)
+    f0, _ = fa.rope_frequencies(128, 10000.0)
+    ratio = f0 / fy
+    turns = 4096 * f0 / (2 * math.pi)
+    assert torch.allclose(ratio[turns > 40], torch.ones(()).double())
+    assert torch.allclose(ratio[turns < 0.8], torch.full((), 8.0).double())
+    assert bool((ratio[1:] >= ratio[:-1] - 1e-12).all())
+    assert abs(ay - (0.1 * math.log(8.0) + 1.0)) < 1e-15
+    for bad in (dict(rotary_dim=7), dict(rotary_dim=0), dict(rotary_dim=64, base=1.0),
+                dict(rotary_dim=64, factor=0.5, scaling="linear"), dict(rotary_dim=64, factor=2.0),
+                dict(rotary_dim=64, scaling="yarn", factor=2.0), dict(rotary_dim=64, scaling="other"),
+                dict(rotary_dim=64, scaling="ntk", factor=2.0, length=8192)):
+        with pytest.raises(ValueError):
+            fa.rope_frequencies(**bad)

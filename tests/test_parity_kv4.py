@@ -1,0 +1,208 @@
+"""The 4-bit cache: append and read bit for bit, decode against the 64-bit form."""
+
+import pytest
+import torch
+
+import _plain as P
+
+pytestmark = pytest.mark.gpu
+
+fa = pytest.importorskip("io_aware_exact_forward_b200")
+
+
+def _rand(shape, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(shape, generator=g).to(torch.bfloat16)
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+def _filled(B, Hkv, Tk, d, seed):
+    """A cache of quantised rows (keys with offsets by channel), and its values in 64 bits."""
+    k = (_rand((B, Hkv, Tk, d), seed).float() + _rand((Hkv, 1, d), seed + 1).float()).to(torch.bfloat16)
+    v = _rand((B, Hkv, Tk, d), seed + 2)
+    cache = fa.KV4Cache(*(t.cuda() for x in (k, v) for t in P.pack4(x)))
+    return cache, P.values4(cache.k_codes, cache.k_params), P.values4(cache.v_codes, cache.v_params)
+
+
+@pytest.mark.parametrize("B,T,Hkv,d,Tk,start,count", [
+    (1, 1, 1, 64, 64, [0], None),
+    (3, 1, 8, 128, 192, [0, 77, 191], None),
+    (2, 50, 2, 64, 128, [3, 100], None),            # the second runs past the cache's end
+    (2, 50, 3, 128, 128, [-10, 60], [50, 17]),      # the first begins before it
+    (2, 5, 2, 128, 64, [1, 2], [0, 9]),             # nothing of the first; a count above T
+    (1, 700, 4, 64, 704, [4], None),
+])
+def test_append_and_read(B, T, Hkv, d, Tk, start, count):
+    k, v = _rand((B, T, Hkv, d), 1), _rand((B, T, Hkv, d), 2)
+    k[:, :, :, 0] *= 30          # an outlier channel
+    k[0, 0, 0, :32] = 1.5        # a group of one value: step 0
+    v[0, 0, 0, :32] = 0
+    cache = fa.kv4_cache(B, Hkv, Tk, d)
+    for t in cache:
+        t.view(torch.uint8).fill_(0xA5)
+    before = [t.cpu().clone() for t in cache]
+    fa.kv4_append(k.cuda(), v.cuda(), cache, _i32(start), None if count is None else _i32(count))
+    assert fa.check() == 0
+    want = [t.clone() for t in before]
+    for b in range(B):
+        for t in range(min(T, T if count is None else count[b])):
+            at = start[b] + t
+            if 0 <= at < Tk:
+                for x, c, p in ((k, 0, 1), (v, 2, 3)):
+                    want[c][b, :, at], want[p][b, :, at] = P.pack4(x[b, t])
+    for got, w in zip(cache, want):
+        assert torch.equal(got.cpu().view(torch.uint8), w.view(torch.uint8))
+    rk, rv = fa.kv4_read(cache, _i32(start), T, None if count is None else _i32(count))
+    assert fa.check() == 0
+    for got, codes, params in ((rk, want[0], want[1]), (rv, want[2], want[3])):
+        ref = torch.zeros((B, T, Hkv, d), dtype=torch.float64)
+        vals = P.values4(codes, params)[0]
+        for b in range(B):
+            for t in range(min(T, T if count is None else count[b])):
+                if 0 <= start[b] + t < Tk:
+                    ref[b, t] = vals[b, :, start[b] + t]
+        assert torch.equal(got.cpu(), ref.float().to(torch.bfloat16))
+
+
+def test_append_takes_slices_and_odd_values():
+    """k and v out of a packed projection; the largest bf16 values, denormals,
+    NaN and infinities keep to their group."""
+    B, T, Hkv, d = 2, 3, 2, 64
+    x = _rand((B, T, 4 + 2 * Hkv, d), 3)
+    big = torch.finfo(torch.bfloat16).max
+    x[0, 0, 4, :32] = (torch.linspace(-1, 1, 32) * big).to(torch.bfloat16)
+    x[0, 1, 4, :32] = torch.arange(32).to(torch.bfloat16) * 2.0 ** -133
+    x[0, 2, 4, 5] = float("nan")
+    x[1, 0, 4, 40] = float("inf")
+    x[1, 1, 4, :32] = 100 + torch.arange(32) * 0.5          # a range far smaller than the offset
+    dev = x.cuda()
+    k, v = dev[:, :, 4:4 + Hkv], dev[:, :, 4 + Hkv:]
+    a, b = fa.kv4_cache(B, Hkv, 64, d), fa.kv4_cache(B, Hkv, 64, d)
+    fa.kv4_append(k, v, a, _i32([0, 9]))
+    fa.kv4_append(k.contiguous(), v.contiguous(), b, _i32([0, 9]))
+    ra, rb = fa.kv4_read(a, _i32([0, 9]), T), fa.kv4_read(b, _i32([0, 9]), T)
+    assert fa.check() == 0
+    for m, n in zip(ra, rb):
+        assert torch.equal(m.view(torch.int16), n.view(torch.int16))
+    got = ra[0].cpu()
+    fine = torch.isfinite(got)
+    bad = torch.zeros_like(fine)
+    bad[0, 2, 0, :32] = True
+    bad[1, 0, 0, 32:] = True
+    assert torch.equal(fine, ~bad)
+    c, s, z = P.split4(x[:, :, 4:4 + Hkv])
+    val = (s.double().repeat_interleave(32, -1) * (c - 8) + z.double().repeat_interleave(32, -1))
+    assert torch.equal(got[fine], val[fine].float().to(torch.bfloat16))
+    # half a step, and the roundings of step and centre, from the input
+    xs = x[:, :, 4:4 + Hkv].double()
+    step = s.double().repeat_interleave(32, -1)
+    lim = (0.5 + 8 * P.H) * step + 2 * P.H * z.double().abs().repeat_interleave(32, -1) + P.H * val.abs() + 2.0 ** -133
+    assert bool(((got.double() - xs).abs() <= lim)[fine].all())
+
+
+DECODE = [
+    # Hq, Hkv, d, Tk, W, S, seqlens
+    (1, 1, 64, 64, 0, 0, [1]),
+    (8, 2, 128, 1024, 0, 0, [0, 1, 15, 16, 63, 64, 65, 128, 1000, 1024]),
+    (4, 4, 64, 576, 0, 0, [575, 576, 3, 512]),
+    (16, 2, 128, 704, 0, 0, [700, 129]),
+    (8, 4, 64, 704, 0, 0, [700, 129]),
+    (8, 2, 128, 1024, 300, 4, [0, 1, 4, 255, 304, 305, 1000]),
+    (4, 4, 64, 1024, 1, 1, [1, 2, 64, 65, 777]),
+    (8, 1, 64, 1024, 64, 130, [1000, 129, 128, 127]),
+    (16, 2, 128, 1024, 513, 0, [3, 1000, 513, 514]),
+    (2, 2, 128, 1024, 5000, 70, [1, 63, 64, 65, 500]),
+    (8, 1, 64, 64, 16, 4, [1 << 20, -5]),                 # lengths outside the cache are clamped
+    (32, 8, 128, 4096, 0, 0, [4096, 2049, 31]),
+]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,Tk,W,S,seqlens", DECODE)
+def test_decode(Hq, Hkv, d, Tk, W, S, seqlens):
+    B = len(seqlens)
+    cache, (kv, _), (vv, vp) = _filled(B, Hkv, Tk, d, 60 + W + d)
+    q = _rand((B, Hq, d), 61)
+    lens = [min(max(n, 0), Tk) for n in seqlens]
+    for b, n in enumerate(lens):
+        # rows that the query does not see hold NaN steps and centres
+        lo = max(0, n - W) if W else 0
+        for p in (cache.k_params, cache.v_params):
+            p[b, :, n:] = float("nan")
+            p[b, :, min(S, lo):lo] = float("nan")
+    o, lse = fa.kv4_decode(q.cuda(), cache, _i32(seqlens), window=W or None, sinks=S)
+    assert fa.check() == 0
+    ref, tol, rl = P.decode(q, kv, vv, vp, lens, W, S, d ** -0.5)
+    P.check(o, ref, tol, "O")
+    P.check_lse(lse, rl)
+    o2, lse2 = fa.kv4_decode(q.cuda(), cache, _i32(seqlens), window=W or None, sinks=S)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2), "the same inputs give the same bits"
+
+
+def test_decode_many_sequences():
+    """More sequences than a block plans at once."""
+    B, Hkv, d, Tk = 1500, 1, 64, 64
+    cache, (kv, _), (vv, vp) = _filled(B, Hkv, Tk, d, 70)
+    q = _rand((B, 2, d), 71)
+    lens = [i * 7 % 65 for i in range(B)]
+    o, lse = fa.kv4_decode(q.cuda(), cache, _i32(lens))
+    assert fa.check() == 0
+    ref, tol, rl = P.decode(q, kv, vv, vp, lens, 0, 0, d ** -0.5)
+    P.check(o, ref, tol, "O")
+    P.check_lse(lse, rl)
+
+
+def test_decode_on_its_own_stream_and_in_graphs():
+    """Two graphs over one cache, replayed in turn after its contents changed,
+    and a call on a side stream."""
+    B, Hkv, Hq, d, Tk = 3, 2, 8, 128, 1024
+    cache, _, _ = _filled(B, Hkv, Tk, d, 80)
+    q1, q2 = _rand((B, Hq, d), 81).cuda(), _rand((B, Hq, d), 82).cuda()
+    lens = _i32([1000, 5, 640])
+    fa.kv4_decode(q1, cache, lens)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        s1 = fa.kv4_decode(q1, cache, lens)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for q in (q1, q2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(fa.kv4_decode(q, cache, lens))
+        graphs.append(g)
+    lens.copy_(_i32([17, 1024, 0]))
+    cache.v_codes.copy_(cache.v_codes.flip(0))
+    for _ in range(2):
+        for g in graphs:
+            g.replay()
+    want = [fa.kv4_decode(q, cache, lens) for q in (q1, q2)]
+    assert fa.check() == 0
+    for a, b in zip(outs, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert bool(torch.isfinite(s1[0].float()).all())
+
+
+def test_bad_calls():
+    cache = fa.kv4_cache(2, 2, 64, 64)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    n = _i32([1, 1])
+    for bad in (dict(q=q[:1]), dict(q=q[:, :3]), dict(seqlens=n[:1]), dict(sinks=2000, window=4),
+                dict(out=q[:, :2]), dict(lse=torch.zeros(1, device="cuda")), dict(scale=float("nan")),
+                dict(workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))):
+        kw = dict(dict(q=q, cache=cache, seqlens=n), **bad)
+        with pytest.raises((ValueError, fa.FAError)):
+            fa.kv4_decode(**kw)
+    with pytest.raises(TypeError):
+        fa.kv4_decode(q, cache, n.long())
+    x = torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        fa.kv4_append(x[:1], x[:1], cache, n)
+    with pytest.raises(ValueError):
+        fa.kv4_append(x, x[:, :2], cache, n)
+    with pytest.raises(TypeError):
+        fa.kv4_append(x, x, cache, None)
+    with pytest.raises(ValueError):
+        fa.kv4_read(fa.KV4Cache(cache[0], cache[1][:, :, :32], cache[2], cache[3]), n, 1)

@@ -1,0 +1,158 @@
+"""Sliding window with sinks: forward, backward (default and deterministic) and
+decode against the 64-bit form."""
+
+import pytest
+import torch
+
+import _plain as P
+
+pytestmark = pytest.mark.gpu
+
+fa = pytest.importorskip("io_aware_exact_forward_b200")
+
+
+def _rand(shape, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(shape, generator=g).to(torch.bfloat16)
+
+
+CASES = [
+    # B, Hq, Hkv, Tq, Tk, d, W, sinks
+    (1, 1, 1, 1, 1, 64, 1, 1),
+    (1, 2, 2, 300, 300, 64, 1, 1),            # the diagonal key and one sink
+    (1, 2, 1, 517, 517, 64, 100, 4),          # sink tile beside window tiles, ragged tail, GQA 2
+    (1, 2, 2, 384, 384, 128, 128, 128),       # sinks of exactly one tile
+    (2, 4, 2, 517, 517, 128, 200, 130),       # sinks into a second tile
+    (1, 2, 2, 200, 450, 64, 130, 3),          # Tq < Tk
+    (1, 2, 2, 450, 200, 128, 64, 5),          # Tq > Tk: early rows see no key
+    (1, 4, 1, 640, 640, 64, 1000, 7),         # window wider than the sequence
+    (1, 8, 1, 512, 512, 64, 257, 1024),       # more sinks than keys, G = 8
+    (1, 1, 1, 1500, 1500, 128, 64, 2),        # sink tile in pieces (12 query tiles, 4 each)
+    (1, 2, 1, 1100, 2300, 64, 60, 200),       # pieces of two sink tiles, Tq < Tk
+]
+
+
+def _inputs(B, Hq, Hkv, Tq, Tk, d, W, S):
+    s = 17 + Tq + 3 * Tk + d + W + 5 * S
+    return (_rand((B, Tq, Hq, d), s), _rand((B, Tk, Hkv, d), s + 1), _rand((B, Tk, Hkv, d), s + 2),
+            _rand((B, Tq, Hq, d), s + 3))
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,Tq,Tk,d,W,S", CASES)
+def test_sink_forward(B, Hq, Hkv, Tq, Tk, d, W, S):
+    q, k, v, _ = _inputs(B, Hq, Hkv, Tq, Tk, d, W, S)
+    o, lse = fa.forward(q.cuda(), k.cuda(), v.cuda(), window=W, sinks=S)
+    assert fa.check() == 0
+    ref, tol, rl = P.sink_forward(q, k, v, W, S, d ** -0.5)
+    P.check(o, ref, tol, "O")
+    P.check_lse(lse, rl)
+
+
+@pytest.mark.parametrize("deterministic", [False, True])
+@pytest.mark.parametrize("B,Hq,Hkv,Tq,Tk,d,W,S", CASES)
+def test_sink_backward(B, Hq, Hkv, Tq, Tk, d, W, S, deterministic):
+    q, k, v, do = _inputs(B, Hq, Hkv, Tq, Tk, d, W, S)
+    c = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.forward(*c[:3], window=W, sinks=S)
+    got = fa.backward(*c[:3], o, lse, c[3], window=W, sinks=S, deterministic=deterministic)
+    assert fa.check() == 0
+    ref = P.sink_backward(q, k, v, do, W, S, d ** -0.5)
+    for n, x in zip(("dq", "dk", "dv"), got):
+        P.check(x, *ref[n], n)
+    if deterministic:
+        again = fa.backward(*c[:3], o, lse, c[3], window=W, sinks=S, deterministic=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_sink_gradient_against_differences():
+    """Directional derivatives of L = sum(dO * O): the 64-bit loss's central
+    difference along u against the kernel's gradients."""
+    B, Hq, Hkv, T, d, W, S = 1, 4, 2, 300, 64, 40, 3
+    q, k, v, do = _inputs(B, Hq, Hkv, T, T, d, W, S)
+    c = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.forward(*c[:3], window=W, sinks=S)
+    got = dict(zip("qkv", fa.backward(*c[:3], o, lse, c[3], window=W, sinks=S)))
+    tol = P.sink_backward(q, k, v, do, W, S, d ** -0.5)
+    G = do.double()
+
+    def loss(q, k, v):
+        return float((P.sink_forward(q, k, v, W, S, d ** -0.5)[0] * G).sum())
+
+    h = 1e-5
+    x = dict(q=q.double(), k=k.double(), v=v.double())
+    for n in "qkv":
+        u = torch.randn(x[n].shape, generator=torch.Generator().manual_seed(9), dtype=torch.float64)
+        up, dn = dict(x), dict(x)
+        up[n], dn[n] = x[n] + h * u, x[n] - h * u
+        diff = (loss(**up) - loss(**dn)) / (2 * h)
+        bound = float((tol["d" + n][1] * u.abs()).sum())   # the gradients' own bound, along u
+        assert abs(float((got[n].double().cpu() * u).sum()) - diff) <= bound + 1e-3, n   # h^2 term
+
+
+def test_zero_sinks_is_the_window():
+    q, k, v, do = (x.cuda() for x in _inputs(1, 2, 2, 300, 300, 64, 100, 0))
+    a, b = fa.forward(q, k, v, window=100), fa.forward(q, k, v, window=100, sinks=0)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_every_key_visible_is_causal():
+    """A window and sinks that leave nothing out: the causal result, bit for bit."""
+    q, k, v, _ = (x.cuda() for x in _inputs(1, 2, 2, 500, 500, 128, 400, 120))
+    a, b = fa.forward(q, k, v, causal=True), fa.forward(q, k, v, window=400, sinks=120)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_sink_forward_persistent_items():
+    """More items than SMs: later items of a CTA, and sampled long rows."""
+    H, T, d, W, S = 16, 4096, 64, 300, 4
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn((1, T, H, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
+    o, lse = fa.forward(q, k, v, window=W, sinks=S)
+    assert fa.check() == 0
+    rows = torch.tensor([0, 3, 127, 128, 299, 300, 304, 2047, 2048, 4095])
+    mask = P.visible(T, T, W, S)[rows]
+    for h in (0, 7, 15):
+        Q, K, V = (x[0, :, h].double().cpu() for x in (q, k, v))
+        ref, rl, _, a = P.attention(Q[rows], K, V, mask, d ** -0.5)
+        P.check(o[0, rows.cuda(), h], ref, (2 * P.H + P.R32) * a + P.H * ref.abs(), f"head {h}")
+        P.check_lse(lse[0, h, rows.cuda()], rl)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,chunk,W,S,seqlens", [
+    (8, 2, 128, 256, 300, 4, [0, 1, 4, 255, 304, 305, 1000]),
+    (4, 4, 64, 256, 1, 1, [1, 2, 64, 65, 777]),
+    (16, 2, 128, 512, 513, 600, [3, 1000, 513, 514]),    # sinks beyond a chunk
+    (2, 2, 64, 64, 5000, 70, [1, 63, 64, 65, 500]),      # wider than every sequence
+    (8, 1, 64, 64, 64, 64, [1000, 129, 128, 127]),
+    (8, 1, 64, 64, 64, 64, [1 << 20, -5]),               # lengths outside the cache are clamped
+])
+def test_sink_decode(Hq, Hkv, d, chunk, W, S, seqlens):
+    B, Tk = len(seqlens), 1000
+    q, k, v = _rand((B, Hq, d), 50 + W), _rand((B, Tk, Hkv, d), 51 + W), _rand((B, Tk, Hkv, d), 52 + W)
+    lens = [min(max(n, 0), Tk) for n in seqlens]
+    kk, vv = k.cuda(), v.cuda()
+    for b, n in enumerate(lens):
+        # rows that the query does not see hold NaN
+        lo = max(0, n - W)
+        for t in (kk, vv):
+            t[b, n:] = float("nan")
+            t[b, min(S, lo):lo] = float("nan")
+    o, lse = fa.decode_splitkv(q.cuda(), kk, vv, torch.tensor(seqlens, dtype=torch.int32).cuda(), chunk=chunk, window=W,
+                               sinks=S)
+    assert fa.check() == 0
+    ref, tol, rl = P.decode(q, k.double().transpose(1, 2), v.double().transpose(1, 2), None, lens, W, S, d ** -0.5)
+    P.check(o, ref, tol, "O")
+    P.check_lse(lse, rl)
+
+
+def test_sink_decode_is_the_last_row_of_the_forward():
+    q, k, v = _rand((1, 700, 4, 128), 1), _rand((1, 700, 2, 128), 2), _rand((1, 700, 2, 128), 3)
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    o, lse = fa.forward(q, k, v, window=150, sinks=9)
+    od, ld = fa.decode_splitkv(q[:, -1].contiguous(), k, v, torch.tensor([700], dtype=torch.int32).cuda(), window=150,
+                               sinks=9)
+    # each within the bound of the same exact row
+    ref, tol, _ = P.sink_forward(q.cpu()[:, -1:], k.cpu(), v.cpu(), 150, 9, 128 ** -0.5)
+    P.check(o[:, -1:], ref, tol, "forward")
+    P.check(od[:, None], ref, tol, "decode")
+    assert float((lse[0, :, -1] - ld[0]).abs().max()) <= 2 * P.LSE_TOL
