@@ -116,6 +116,7 @@ template <int D, int G>
 static int decode_setup_one() {
   int st = set_smem(fa_decode_split_kernel<D, G>, DecCfg<D, G>::SMEM_BYTES);
   if (!st) st = set_smem(fa_decode_split_kernel<D, G, true>, DecCfg<D, G>::SMEM_BYTES);
+  if (!st) st = set_smem(fa_kv4_split_kernel<D, G>, Kv4Cfg<D, G>::SMEM_BYTES);
   return st;
 }
 
@@ -1210,13 +1211,47 @@ extern "C" int fa_kv4_read(void* k, void* v, const void* k_codes, const void* k_
 }
 
 namespace fa {
-static constexpr int kKv4Chunk = 512;
+
+// Codes as [pairs][Tk][d/2] bytes with box {d/2, 64, 1}, in the swizzle of
+// their row width.
+static int kv4_tmap(CUtensorMap* m, const void* base, uint64_t pairs, uint64_t Tk, int d) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return FA_ERR_CUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)d / 2, Tk, pairs};
+  const cuuint64_t strides[2] = {(cuuint64_t)d / 2, Tk * (d / 2)};
+  const cuuint32_t box[3] = {(cuuint32_t)d / 2, 64, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+// Workspace pieces: prefix, then (maximum, sum), then O of every slot.
+struct Kv4Ws {
+  size_t ml, o, bytes;
+};
+static Kv4Ws kv4_ws(int B, int Hq, int Hkv, int d) {
+  const size_t nb = std::min(B, kKv4MaxSeqs);
+  const size_t rows = (nb * Hkv + kKv4MaxGrid) * (Hq / Hkv);
+  Kv4Ws w;
+  w.ml = round256((nb + 1) * 4);
+  w.o = w.ml + round256(rows * 8);
+  w.bytes = w.o + round256(rows * d * 4);
+  return w;
+}
+
+template <int D, int G>
+static int kv4_launch(const Kv4DecodeParams& p, cudaStream_t s) {
+  fa_kv4_split_kernel<D, G><<<p.n_cta, Kv4Cfg<D, G>::THREADS, Kv4Cfg<D, G>::SMEM_BYTES, s>>>(p);
+  return launch_status();
+}
+
 }  // namespace fa
 
 extern "C" size_t fa_kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int Tk_max, int d) {
-  if (B < 0 || Hq < 1 || Hkv < 1 || Tk_max < 0 || (d != 64 && d != 128)) return 0;
-  const size_t n = ((size_t)Tk_max + kKv4Chunk - 1) / kKv4Chunk;
-  return round256((size_t)B * Hq * n * d * 4) + round256((size_t)B * Hq * n * 8);
+  if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Tk_max < 0 || (d != 64 && d != 128)) return 0;
+  return kv4_ws(B, Hq, Hkv, d).bytes;
 }
 
 extern "C" int fa_kv4_decode(const void* q, const void* k_codes, const void* k_params, const void* v_codes,
@@ -1230,37 +1265,49 @@ extern "C" int fa_kv4_decode(const void* q, const void* k_codes, const void* k_p
     return FA_ERR_INVALID_ARG;
   const int G = Hq / Hkv;
   if (G != 1 && G != 2 && G != 4 && G != 8) return FA_ERR_UNSUPPORTED;
-  if ((int64_t)B * Hq > (1 << 26) || (int64_t)B * Hkv > 65535) return FA_ERR_INVALID_ARG;
+  // tiles of the list and (sequence, KV head) pairs are counted in 31 bits
+  if ((int64_t)B * Hq > (1 << 26) || (int64_t)B * Hkv * (Tk_max / 64) > (1 << 30)) return FA_ERR_INVALID_ARG;
   if (B == 0) return FA_OK;
   if (!q || !seqlens_k || !o || !lse) return FA_ERR_INVALID_ARG;
   if (Tk_max > 0 && (st = kv4_check_cache(k_codes, k_params, v_codes, v_params))) return st;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(seqlens_k) & 3u))
     return FA_ERR_ALIGNMENT;
-  if (!ws || ws_bytes < fa_kv4_decode_workspace_bytes(B, Hq, Hkv, Tk_max, d) || !aligned16(ws))
-    return FA_ERR_WORKSPACE;
+  const Kv4Ws w = kv4_ws(B, Hq, Hkv, d);
+  if (!ws || ws_bytes < w.bytes || !aligned16(ws)) return FA_ERR_WORKSPACE;
   if ((st = device_setup())) return st;
+  int nsm = 0;
+  if ((st = sm_count(&nsm))) return st;
   Kv4DecodeParams p;
   memset(&p, 0, sizeof(p));
-  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
-  p.k_codes = reinterpret_cast<const uint8_t*>(k_codes);
-  p.v_codes = reinterpret_cast<const uint8_t*>(v_codes);
+  if (Tk_max > 0) {
+    st = kv4_tmap(&p.tm_k, k_codes, (uint64_t)B * Hkv, Tk_max, d);
+    if (!st) st = kv4_tmap(&p.tm_v, v_codes, (uint64_t)B * Hkv, Tk_max, d);
+    if (st) return st;
+  }
+  uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+  p.ws_prefix = reinterpret_cast<int*>(base);
+  p.ws_ml = reinterpret_cast<float*>(base + w.ml);
+  p.ws_o = reinterpret_cast<float*>(base + w.o);
   p.k_params = reinterpret_cast<const __nv_bfloat16*>(k_params);
   p.v_params = reinterpret_cast<const __nv_bfloat16*>(v_params);
-  p.seqlens = seqlens_k;
-  p.chunk = kKv4Chunk;
-  p.nsplit = (Tk_max + kKv4Chunk - 1) / kKv4Chunk;
-  p.ws_o = reinterpret_cast<float*>(ws);
-  p.ws_ml = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + round256((size_t)B * Hq * p.nsplit * d * 4));
-  p.o = reinterpret_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Tk_max = Tk_max;
+  p.Hq = Hq; p.Hkv = Hkv; p.Tk_max = Tk_max;
   p.window = window;
   p.sinks = sinks;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.wait_limit_ns = kWaitLimitNs;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (p.nsplit > 0) {
-    const dim3 grid((unsigned)p.nsplit, (unsigned)(B * Hkv));
-#define FA_KV4_LAUNCH(DD, GG) fa_kv4_split_kernel<DD, GG><<<grid, 128, 0, s>>>(p)
+  for (int b0 = 0; b0 < B; b0 += kKv4MaxSeqs) {
+    p.B = std::min(B - b0, kKv4MaxSeqs);
+    p.pair0 = b0 * Hkv;
+    p.q = reinterpret_cast<const __nv_bfloat16*>(q) + (size_t)b0 * Hq * d;
+    p.seqlens = seqlens_k + b0;
+    p.o = reinterpret_cast<__nv_bfloat16*>(o) + (size_t)b0 * Hq * d;
+    p.lse = lse + (size_t)b0 * Hq;
+    // no more blocks than the longest possible list has tiles
+    const long long tiles = (long long)p.B * Hkv * (Tk_max / 64);
+#define FA_KV4_LAUNCH(DD, GG)                                                                                   \
+    (p.n_cta = (int)std::min({(long long)nsm * Kv4Cfg<DD, GG>::CTAS, (long long)kKv4MaxGrid, std::max(tiles, 1ll)}), \
+     st = kv4_launch<DD, GG>(p, s))
     if (d == 64) {
       if (G == 1) FA_KV4_LAUNCH(64, 1); else if (G == 2) FA_KV4_LAUNCH(64, 2);
       else if (G == 4) FA_KV4_LAUNCH(64, 4); else FA_KV4_LAUNCH(64, 8);
@@ -1269,12 +1316,13 @@ extern "C" int fa_kv4_decode(const void* q, const void* k_codes, const void* k_p
       else if (G == 4) FA_KV4_LAUNCH(128, 4); else FA_KV4_LAUNCH(128, 8);
     }
 #undef FA_KV4_LAUNCH
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (st) return st;
+    const unsigned blocks = (unsigned)(((size_t)p.B * Hq * 32 + 255) / 256);
+    if (d == 64)
+      fa_kv4_combine_kernel<64><<<blocks, 256, 0, s>>>(p);
+    else
+      fa_kv4_combine_kernel<128><<<blocks, 256, 0, s>>>(p);
+    if ((st = launch_status())) return st;
   }
-  const unsigned blocks = (unsigned)(((size_t)B * Hq * 32 + 255) / 256);
-  if (d == 64)
-    fa_kv4_combine_kernel<64><<<blocks, 256, 0, s>>>(p);
-  else
-    fa_kv4_combine_kernel<128><<<blocks, 256, 0, s>>>(p);
-  return launch_status();
+  return FA_OK;
 }

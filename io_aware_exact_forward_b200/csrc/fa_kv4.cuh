@@ -16,6 +16,7 @@
 // overflow.  A group that holds a NaN or an infinity reads back non-finite.
 #pragma once
 
+#include "fa_decode.cuh"
 #include "fa_ptx.cuh"
 
 namespace fa {
@@ -143,130 +144,532 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
 // ---------------------------------------------------------------------------
 // decode
 // ---------------------------------------------------------------------------
+// With u = code as an integer 0..15 and s, z of key j and group c,
+//   S_j = scale sum_c ( s_jc sum_{i in c} q_i (u_ij - 8) + z_jc sum_{i in c} q_i ),
+//   O_i = sum_j ( p_j s_jc (u_ij - 8) + p_j z_jc ) / l       (i in group c),
+// so the steps never touch the d codes of a row: they scale 32-bit sums of four
+// group products of a score, and the probabilities on the way into P V.
+//
+// On the tensor cores (mma.sync m16n8k16; a decode has too few rows for a
+// tcgen05 tile) a code enters K's product as the bf16 128 + u, which is a mask
+// and an OR of its nibble, exact, with no conversion; the 136 = 128 + 8 is taken
+// off by starting the score's accumulator at -136 sum q.  V's codes enter as
+// u - 8, one more (exact) bf16 subtraction: taking 136 sum p s off O's sums
+// instead loses what averaging over a long sequence leaves of O (measured 0.9%
+// of O's norm at 17k keys, against 0.2%).  The centres' parts are two small
+// products of their own: z against sum q (split into three bf16 parts, 24
+// bits), and p against z.  p s is formed in 32 bits and rounded to bf16 once; l
+// sums the unrounded p.
+//
+// Operand layouts.  A 16-byte chunk of a row's codes is one group.  For K,
+// ldmatrix gives lane (g, t) of a warp the word of key g's dims 8t .. 8t + 7 of
+// the group: nibble k of its halves is the pair of dims (8t + k, 8t + 4 + k),
+// and Q is permuted to match.  For V, ldmatrix.trans gives keys 2t and 2t + 1
+// (the halves) at dims 4g .. 4g + 3: nibble k is the pair of keys that P^T's
+// operand wants, so V^T enters as the row operand, 16 dims by 16 keys, and P^T
+// as the column operand: both come out of the score's accumulator in place.
+//
+// Work.  A persistent grid; every sequence's visible 64-key tiles, in the order
+// of (sequence, KV head), are one long list that the blocks share out evenly
+// whatever the lengths are.  A block's stretch of one (sequence, KV head) ends
+// in a partial result (slot: block + pair, both grow along the list), and a
+// second kernel joins them.
+static constexpr int kKv4MaxSeqs = 1024;  // sequences per launch
+static constexpr int kKv4MaxGrid = 512;
+
 struct Kv4DecodeParams {
+  CUtensorMap tm_k;        // codes [B * Hkv][Tk_max][d/2] bytes, box {d/2, 64, 1}, swizzled
+  CUtensorMap tm_v;
   const __nv_bfloat16* q;  // [B][Hq][d]
-  const uint8_t* k_codes;  // [B][Hkv][Tk_max][d/2]
-  const uint8_t* v_codes;
   const __nv_bfloat16* k_params;  // [B][Hkv][Tk_max][2 d/32]
   const __nv_bfloat16* v_params;
   const int* seqlens;      // [B]
-  float* ws_o;             // [B * Hkv][nsplit][G][d], O scaled by its own maximum
-  float* ws_ml;            // [B * Hkv][nsplit][G][2], maximum (log2 units) and sum
+  int* ws_prefix;          // [B + 1] visible tiles before sequence b
+  float* ws_ml;            // [slot][G][2], maximum (log2 units) and sum
+  float* ws_o;             // [slot][G][d], unnormalised
   __nv_bfloat16* o;        // [B][Hq][d]
   float* lse;              // [B][Hq]
-  int B, Hq, Hkv, Tk_max, nsplit, chunk;
+  int B, Hq, Hkv, Tk_max;
+  int pair0;               // (sequence, KV head) pairs before this launch's in the cache
+  int n_cta;
   int window, sinks;       // window > 0: only the last `window` keys and the first `sinks`
   float scale_log2;
+  unsigned long long wait_limit_ns;
 };
 
-__device__ __forceinline__ int kv4_len(const Kv4DecodeParams& p, int b) { return min(max(p.seqlens[b], 0), p.Tk_max); }
+// Visible tiles of a sequence: 0 .. n_sink - 1, then lo_tile ..; `count` in all.
+struct Kv4Seq {
+  int len, lo, n_sink, lo_tile, count;
+  __device__ __forceinline__ Kv4Seq(const Kv4DecodeParams& p, int seqlen) {
+    len = min(max(seqlen, 0), p.Tk_max);
+    lo = p.window > 0 ? max(0, len - p.window) : 0;
+    const int end = (len + 63) >> 6;
+    n_sink = min(end, (p.sinks + 63) >> 6);
+    lo_tile = max(n_sink, lo >> 6);
+    count = n_sink + max(0, end - lo_tile);
+  }
+  __device__ __forceinline__ int tile(int j) const { return j < n_sink ? j : lo_tile + j - n_sink; }
+};
 
-// One block per (chunk, sequence and KV head): four warps take the chunk's
-// keys in turn, each lane d / 32 dims of all G query heads.
 template <int D, int G>
-__global__ void __launch_bounds__(128) fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
-  constexpr int E = D / 32, NG = D / kKv4Group;
-  __shared__ float so[4][G][D];
-  __shared__ float sml[4][G][2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bh = blockIdx.y, b = bh / p.Hkv, hkv = bh % p.Hkv;
-  const int len = kv4_len(p, b);
-  const int lo = p.window > 0 ? max(0, len - p.window) : 0;
-  const int k0 = blockIdx.x * p.chunk, k1 = min(k0 + p.chunk, len);
-  float q[G][E], o[G][E], m[G], l[G];
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      q[g][e] = __bfloat162float(p.q[((size_t)b * p.Hq + hkv * G + g) * D + lane * E + e]);
-      o[g][e] = 0.f;
-    }
-  }
-  for (int key = k0 + warp; key < k1; key += 4) {
-    if (key < lo && key >= p.sinks) continue;
-    const size_t r = (size_t)bh * p.Tk_max + key;
-    float kv[2][E];
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint8_t* c = (w ? p.v_codes : p.k_codes) + r * (D / 2) + lane * (E / 2);
-      const __nv_bfloat16* pr = (w ? p.v_params : p.k_params) + r * 2 * NG + lane * E / kKv4Group;
-      const float s = __bfloat162float(pr[0]), z = __bfloat162float(pr[NG]);
-#pragma unroll
-      for (int e = 0; e < E; ++e) kv[w][e] = fmaf(s, (float)((c[e >> 1] >> (4 * (e & 1))) & 15) - 8.f, z);
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      float d = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) d = fmaf(q[g][e], kv[0][e], d);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-      d *= p.scale_log2;
-      const float mn = fmaxf(m[g], d);
-      const float ref = mn == -INFINITY ? 0.f : mn;  // a NaN score stays one
-      const float a = ex2_approx(m[g] - ref);
-      const float w = ex2_approx(d - ref);
-      m[g] = mn;
-      l[g] = fmaf(l[g], a, w);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[g][e] = fmaf(w, kv[1][e], o[g][e] * a);
-    }
-  }
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][g][lane * E + e] = o[g][e];
-    if (lane == 0) {
-      sml[warp][g][0] = m[g];
-      sml[warp][g][1] = l[g];
-    }
-  }
-  __syncthreads();
-  const size_t slot = (size_t)bh * p.nsplit + blockIdx.x;
-  for (int i = threadIdx.x; i < G * D; i += 128) {
-    const int g = i / D, e = i % D;
-    float M = -INFINITY, L = 0.f, O = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, sml[w][g][0]);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float f = sml[w][g][0] == -INFINITY ? 0.f : ex2_approx(sml[w][g][0] - M);
-      L = fmaf(f, sml[w][g][1], L);
-      O = fmaf(f, so[w][g][e], O);
-    }
-    p.ws_o[(slot * G + g) * D + e] = O;
-    if (e == 0) {
-      p.ws_ml[(slot * G + g) * 2] = M;
-      p.ws_ml[(slot * G + g) * 2 + 1] = L;
-    }
+struct Kv4Cfg {
+  static constexpr int TILE = 64;                     // keys per stage
+  static constexpr int NWARP = 4;                     // compute warps, 16 keys each
+  static constexpr int THREADS = (NWARP + 1) * 32;
+  static constexpr int CB = D / 2, NG = D / kKv4Group, PB = 4 * NG;  // bytes of a row's codes, groups, bytes of params
+  static constexpr int OFF_K = 0, OFF_V = TILE * CB, OFF_KP = 2 * TILE * CB, OFF_VP = OFF_KP + TILE * PB;
+  static constexpr int STAGE_BYTES = OFF_VP + TILE * PB;
+  static constexpr int NSTAGE = (D == 128) ? 5 : 10;
+  static constexpr int OFF_MRG = NSTAGE * STAGE_BYTES;           // [NWARP][G][D] fp32
+  static constexpr int OFF_ML = OFF_MRG + NWARP * G * D * 4;     // m, l: [NWARP][8] each
+  static constexpr int OFF_PRE = OFF_ML + 2 * NWARP * 8 * 4;     // prefix [kKv4MaxSeqs + 1]
+  static constexpr int OFF_SCAN = OFF_PRE + (kKv4MaxSeqs + 4) * 4;
+  static constexpr int OFF_BAR = OFF_SCAN + 64;
+  static constexpr int OFF_FLAG = OFF_BAR + 2 * NSTAGE * 8;
+  static constexpr int SMEM_BYTES = OFF_FLAG + 16 + 1024;        // + alignment slack
+  static constexpr int CTAS = 3;                                 // per SM
+  static constexpr float RESCALE_THRESHOLD = 8.0f;
+  static_assert(STAGE_BYTES % 1024 == 0 && OFF_V % 1024 == 0, "swizzled tiles need their alignment");
+};
+
+// Byte offset of 16-byte chunk c of row r of a code tile (the 64-byte swizzle
+// for 64-byte rows, the 32-byte one for 32-byte rows).
+template <int D>
+__device__ __forceinline__ uint32_t kv4_swz(int r, int c) {
+  if constexpr (D == 128) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  return (uint32_t)(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
+}
+
+// Nibble k of both halves as the bf16 pair 128 + u.
+__device__ __forceinline__ uint32_t kv4_pair(uint32_t w, int k) { return ((w >> (4 * k)) & 0x000F000Fu) | 0x43004300u; }
+
+// The same as u - 8.
+__device__ __forceinline__ uint32_t kv4_pair_c(uint32_t w, int k) {
+  const uint32_t u = kv4_pair(w, k), m136 = 0x43084308u;
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&m136));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ void ldsm_x2_t(uint32_t addr, uint32_t& r0, uint32_t& r1) {
+  asm volatile("ldmatrix.sync.aligned.x2.trans.m8n8.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
+  return r;
+}
+
+// The steps of one row's params, as words of two.
+template <int NG>
+__device__ __forceinline__ void kv4_steps(uint32_t addr, uint32_t (&w)[NG / 2]) {
+  if constexpr (NG == 4) {
+    const uint2 v = lds64(addr);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    w[0] = lds32(addr);
   }
 }
 
-// One warp per (sequence, query head): the chunks' results joined.
+// One stretch of the tile list within one (sequence, KV head).
+struct Kv4Segment {
+  int b, hkv, first, n;  // sequence, KV head, first visible tile (index), tiles
+  __device__ __forceinline__ Kv4Segment(const int* pre, int B, int Hkv, long long at, long long end) {
+    // the sequence whose tiles hold `at`: the last b with pre[b] * Hkv <= at
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((long long)pre[mid] * Hkv <= at) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    const int count = pre[b + 1] - pre[b];
+    const int off = (int)(at - (long long)pre[b] * Hkv);
+    hkv = off / count;
+    first = off - hkv * count;
+    n = (int)min((long long)(count - first), end - at);
+  }
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(Kv4Cfg<D, G>::THREADS, Kv4Cfg<D, G>::CTAS)
+fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
+  using C = Kv4Cfg<D, G>;
+  constexpr int NG = C::NG;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  float* mrg = reinterpret_cast<float*>(smem + C::OFF_MRG);
+  float* m_s = reinterpret_cast<float*>(smem + C::OFF_ML);
+  float* l_s = m_s + C::NWARP * 8;
+  int* pre = reinterpret_cast<int*>(smem + C::OFF_PRE);
+  int* scan = reinterpret_cast<int*>(smem + C::OFF_SCAN);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);
+  volatile int* stop_flag = abort_flag + 1;
+  auto bar_full = [&](int s) { return sbase + C::OFF_BAR + 8u * s; };
+  auto bar_empty = [&](int s) { return sbase + C::OFF_BAR + 8u * (C::NSTAGE + s); };
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  WaitCtl wc{abort_flag, p.wait_limit_ns};
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    *stop_flag = 0;
+    for (int s = 0; s < C::NSTAGE; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), C::NWARP);
+    }
+    fence_barrier_init();
+  }
+  // ---- prefix sum of the sequences' visible tiles, the same in every block
+  {
+    constexpr int PER = (kKv4MaxSeqs + C::THREADS - 1) / C::THREADS;
+    const int i0 = threadIdx.x * PER;
+    int cnt[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      cnt[i] = i0 + i < p.B ? Kv4Seq(p, p.seqlens[i0 + i]).count : 0;
+      sum += cnt[i];
+    }
+    int inc = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += v;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int base = inc - sum;
+    for (int w = 0; w < warp; ++w) base += scan[w];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (i0 + i <= p.B) {
+        pre[i0 + i] = base;
+        if (blockIdx.x == 0) p.ws_prefix[i0 + i] = base;
+      }
+      base += cnt[i];
+    }
+  }
+  __syncthreads();
+  const long long total = (long long)pre[p.B] * p.Hkv;
+  const int n_cta = (int)min((long long)p.n_cta, total);
+  if ((int)blockIdx.x >= n_cta) return;
+  const long long t_begin = total * blockIdx.x / n_cta, t_end = total * (blockIdx.x + 1) / n_cta;
+
+  if (warp == C::NWARP) {
+    // ---------------------------------------------------------- producer
+    if (lane == 0) {
+      tma_prefetch_desc(&p.tm_k);
+      tma_prefetch_desc(&p.tm_v);
+      bool ok = true;
+      int t = 0;
+      for (long long at = t_begin; at < t_end && ok;) {
+        const Kv4Segment sg(pre, p.B, p.Hkv, at, t_end);
+        const Kv4Seq sq(p, p.seqlens[sg.b]);
+        const int pair = p.pair0 + sg.b * p.Hkv + sg.hkv;
+        for (int j = 0; j < sg.n; ++j, ++t) {
+          const int s = t % C::NSTAGE;
+          const int k0 = sq.tile(sg.first + j) * C::TILE;
+          if (t >= C::NSTAGE) ok = mbar_wait(bar_empty(s), (t / C::NSTAGE - 1) & 1, wc);
+          if (!ok) break;
+          const uint32_t st = sbase + s * C::STAGE_BYTES;
+          const size_t row = (size_t)pair * p.Tk_max + k0;
+          mbar_arrive_expect_tx(bar_full(s), C::STAGE_BYTES);
+          tma_load_3d(st + C::OFF_K, &p.tm_k, bar_full(s), 0, k0, pair);
+          bulk_load(st + C::OFF_KP, p.k_params + row * 2 * NG, C::TILE * C::PB, bar_full(s));
+          tma_load_3d(st + C::OFF_V, &p.tm_v, bar_full(s), 0, k0, pair);
+          bulk_load(st + C::OFF_VP, p.v_params + row * 2 * NG, C::TILE * C::PB, bar_full(s));
+        }
+        at += sg.n;
+      }
+      if (!ok)  // every copy already issued lands before the block can exit
+        for (int k = max(0, t - C::NSTAGE); k < t; ++k)
+          mbar_wait_drain(bar_full(k % C::NSTAGE), (k / C::NSTAGE) & 1, p.wait_limit_ns);
+    }
+    return;  // no named barrier below
+  }
+
+  // ------------------------------------------------------------ compute
+  const int g = lane >> 2, t4 = lane & 3;
+  const int kw = warp * 16;  // this warp's 16 keys of every tile
+  bool ok = true;
+  int t = 0;
+  for (long long at = t_begin; at < t_end;) {
+    const Kv4Segment sg(pre, p.B, p.Hkv, at, t_end);
+    const Kv4Seq sq(p, p.seqlens[sg.b]);
+    at += sg.n;
+
+    // Q as the row operand: row g, dims of group c in the order the codes have
+    uint32_t qa[NG][4];
+    float qinit[NG];      // -136 sum of the group's q
+    uint32_t za0, za2 = 0u;
+    {
+      const __nv_bfloat16* qrow = p.q + ((size_t)sg.b * p.Hq + sg.hkv * G + (g < G ? g : 0)) * D;
+      float qs[NG];
+#pragma unroll
+      for (int c = 0; c < NG; ++c) {
+        uint4 v = *reinterpret_cast<const uint4*>(qrow + 32 * c + 8 * t4);
+        if (g >= G) v = make_uint4(0u, 0u, 0u, 0u);
+        qa[c][0] = __byte_perm(v.x, v.z, 0x5410);
+        qa[c][1] = __byte_perm(v.x, v.z, 0x7632);
+        qa[c][2] = __byte_perm(v.y, v.w, 0x5410);
+        qa[c][3] = __byte_perm(v.y, v.w, 0x7632);
+        float q8 = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) +
+                   ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
+        q8 += __shfl_xor_sync(0xffffffffu, q8, 1);
+        q8 += __shfl_xor_sync(0xffffffffu, q8, 2);
+        qs[c] = q8;
+        qinit[c] = -136.f * q8;
+      }
+      // sum q of every group in three bf16 parts: columns (part, group) of the
+      // row operand that meets the centres
+      uint32_t part[3][NG / 2];
+#pragma unroll
+      for (int c = 0; c < NG; c += 2) {
+        float x = qs[c], y = qs[c + 1];
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+          const uint32_t w = pack_bf16x2(x, y);
+          part[n][c / 2] = w;
+          x -= bf16_lo(w);
+          y -= bf16_hi(w);
+        }
+      }
+      if constexpr (NG == 4) {
+        za0 = t4 == 0 ? part[0][0] : t4 == 1 ? part[0][1] : t4 == 2 ? part[1][0] : part[1][1];
+        za2 = t4 == 0 ? part[2][0] : t4 == 1 ? part[2][1] : 0u;
+      } else {
+        za0 = t4 == 0 ? part[0][0] : t4 == 1 ? part[1][0] : t4 == 2 ? part[2][0] : 0u;
+      }
+    }
+
+    float m_run = -INFINITY, l_part = 0.f;   // row g
+    float oacc[NG][2][4];                    // dims 32c + 4g + 2kk (+1), queries 2t, 2t + 1
+    float zacc[4] = {0.f, 0.f, 0.f, 0.f};    // sum of p z, by group
+#pragma unroll
+    for (int c = 0; c < NG; ++c)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) oacc[c][k][e] = 0.f;
+
+    for (int j = 0; j < sg.n; ++j, ++t) {
+      const int s = t % C::NSTAGE;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_full(s), (t / C::NSTAGE) & 1, wc));
+      if (ok) {
+        const uint32_t st = sbase + s * C::STAGE_BYTES;
+        const int key0 = sq.tile(sg.first + j) * C::TILE;
+        const bool whole = key0 + C::TILE <= sq.len && (key0 >= sq.lo || key0 + C::TILE <= p.sinks);
+        auto visible = [&](int key) { return key < sq.len && (key >= sq.lo || key < p.sinks); };
+        if (!whole) {
+          // A masked key's p is 0, but 0 times what an unwritten row's params
+          // may hold (NaN, infinity) is not: zero them.
+          if (lane < 16 && !visible(key0 + kw + lane)) {
+            uint32_t* row = reinterpret_cast<uint32_t*>(smem + s * C::STAGE_BYTES + C::OFF_VP + (kw + lane) * C::PB);
+#pragma unroll
+            for (int i = 0; i < C::PB / 4; ++i) row[i] = 0u;
+          }
+          fence_proxy_async_smem();  // before the next bulk load into this stage
+          __syncwarp();
+        }
+
+        // ---- scores of row g against keys kw + 8 nb + 2t (+1)
+        uint32_t kc[2][NG];
+        if constexpr (D == 128) {
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb)
+            ldsm_x4(st + C::OFF_K + kv4_swz<D>(kw + 8 * nb + (lane & 7), lane >> 3), kc[nb][0], kc[nb][1], kc[nb][2],
+                    kc[nb][3]);
+        } else {
+          ldsm_x4(st + C::OFF_K + kv4_swz<D>(kw + ((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1), kc[0][0],
+                  kc[0][1], kc[1][0], kc[1][1]);
+        }
+        float sc[4];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+          const uint32_t kp = st + C::OFF_KP + (kw + 8 * nb) * C::PB;
+          const uint32_t zw = lds32(kp + g * C::PB + 2 * NG + (NG == 4 ? 4 * (t4 & 1) : 0));
+          uint32_t s0[NG / 2], s1[NG / 2];
+          kv4_steps<NG>(kp + (2 * t4) * C::PB, s0);
+          kv4_steps<NG>(kp + (2 * t4 + 1) * C::PB, s1);
+          float sz[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_16816(sz, za0, 0u, za2, 0u, zw, zw);
+          float2 tot = make_float2(sz[0], sz[1]);
+#pragma unroll
+          for (int c = 0; c < NG; ++c) {
+            float a[4] = {qinit[c], qinit[c], 0.f, 0.f};
+            const uint32_t w = kc[nb][c];
+            mma_16816(a, qa[c][0], 0u, qa[c][1], 0u, kv4_pair(w, 0), kv4_pair(w, 1));
+            mma_16816(a, qa[c][2], 0u, qa[c][3], 0u, kv4_pair(w, 2), kv4_pair(w, 3));
+            const float2 ss = (c & 1) ? make_float2(bf16_hi(s0[c / 2]), bf16_hi(s1[c / 2]))
+                                      : make_float2(bf16_lo(s0[c / 2]), bf16_lo(s1[c / 2]));
+            tot = __ffma2_rn(ss, make_float2(a[0], a[1]), tot);
+          }
+          sc[2 * nb] = tot.x * p.scale_log2;
+          sc[2 * nb + 1] = tot.y * p.scale_log2;
+        }
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!visible(key0 + kw + 8 * (e >> 1) + 2 * t4 + (e & 1))) sc[e] = -INFINITY;
+        }
+
+        // ---- online softmax with a lazily moved reference, as elsewhere
+        float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const bool move = mx > m_run + C::RESCALE_THRESHOLD || (m_run == -INFINITY && mx != -INFINITY);
+        if (__any_sync(0xffffffffu, move)) {
+          float alpha = 1.f;
+          if (move) {
+            alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - mx);
+            m_run = mx;
+            l_part *= alpha;
+          }
+          const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t4);      // row 2t
+          const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);  // row 2t + 1
+#pragma unroll
+          for (int c = 0; c < NG; ++c)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) oacc[c][k][e] *= (e & 1) ? a1 : a0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) zacc[e] *= (e & 1) ? a1 : a0;
+        }
+        const float ref = m_run == -INFINITY ? 0.f : m_run;
+        float pv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          pv[e] = ex2_approx(sc[e] - ref);
+          l_part += pv[e];
+        }
+
+        // ---- O^T += V^T P^T
+        const uint32_t vp = st + C::OFF_VP + kw * C::PB;
+        uint32_t sv[4][NG / 2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kv4_steps<NG>(vp + (8 * (e >> 1) + 2 * t4 + (e & 1)) * C::PB, sv[e]);
+        {
+          uint32_t z0, z1;
+          if constexpr (NG == 4) {
+            // row g: the steps (0..3, not wanted) and the centres (4..7)
+            ldsm_x2_t(vp + (lane & 15) * C::PB, z0, z1);
+          } else {
+            const uint32_t a = vp + 2 * t4 * C::PB + 4;  // the centres' words of keys 2t, 2t + 1 (+ 8)
+            const uint32_t sel = g == 0 ? 0x5410u : 0x7632u;
+            z0 = __byte_perm(lds32(a), lds32(a + C::PB), sel);
+            z1 = __byte_perm(lds32(a + 8 * C::PB), lds32(a + 9 * C::PB), sel);
+            if (g > 1) z0 = z1 = 0u;
+          }
+          mma_16816(zacc, z0, 0u, z1, 0u, pack_bf16x2(pv[0], pv[1]), pack_bf16x2(pv[2], pv[3]));
+        }
+#pragma unroll
+        for (int c2 = 0; c2 < NG; c2 += 2) {
+          uint32_t vc[2][2];  // [group of the two][keys 0..7, 8..15]
+          ldsm_x4_t(st + C::OFF_V + kv4_swz<D>(kw + ((lane >> 3) & 1) * 8 + (lane & 7), c2 + (lane >> 4)), vc[0][0],
+                    vc[0][1], vc[1][0], vc[1][1]);
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            const int c = c2 + cc;
+            float ps[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ps[e] = pv[e] * (cc ? bf16_hi(sv[e][c2 / 2]) : bf16_lo(sv[e][c2 / 2]));
+            const uint32_t b0 = pack_bf16x2(ps[0], ps[1]), b1 = pack_bf16x2(ps[2], ps[3]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              mma_16816(oacc[c][k], kv4_pair_c(vc[cc][0], 2 * k), kv4_pair_c(vc[cc][0], 2 * k + 1),
+                        kv4_pair_c(vc[cc][1], 2 * k), kv4_pair_c(vc[cc][1], 2 * k + 1), b0, b1);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_empty(s));
+    }
+
+    // ---- the four warps' results, joined
+    float l_row = l_part + __shfl_xor_sync(0xffffffffu, l_part, 1);
+    l_row += __shfl_xor_sync(0xffffffffu, l_row, 2);
+    if (t4 == 0) {
+      m_s[warp * 8 + g] = m_run;
+      l_s[warp * 8 + g] = l_row;
+    }
+#pragma unroll
+    for (int c = 0; c < NG; ++c) {
+      const int zrow = NG == 4 ? 4 + c : c;
+      const float add0 = __shfl_sync(0xffffffffu, zacc[0], 4 * zrow + t4);
+      const float add1 = __shfl_sync(0xffffffffu, zacc[1], 4 * zrow + t4);
+      if (2 * t4 < G)
+        *reinterpret_cast<float4*>(&mrg[(warp * G + 2 * t4) * D + 32 * c + 4 * g]) =
+            make_float4(oacc[c][0][0] + add0, oacc[c][0][2] + add0, oacc[c][1][0] + add0, oacc[c][1][2] + add0);
+      if (2 * t4 + 1 < G)
+        *reinterpret_cast<float4*>(&mrg[(warp * G + 2 * t4 + 1) * D + 32 * c + 4 * g]) =
+            make_float4(oacc[c][0][1] + add1, oacc[c][0][3] + add1, oacc[c][1][1] + add1, oacc[c][1][3] + add1);
+    }
+    named_bar_sync(1, C::NWARP * 32);
+    const size_t slot = (size_t)blockIdx.x + sg.b * p.Hkv + sg.hkv;
+    for (int idx = threadIdx.x; idx < G * D; idx += C::NWARP * 32) {
+      const int gg = idx / D, dd = idx % D;
+      float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::NWARP; ++w) M = fmaxf(M, m_s[w * 8 + gg]);
+#pragma unroll
+      for (int w = 0; w < C::NWARP; ++w) {
+        const float f = m_s[w * 8 + gg] == -INFINITY ? 0.f : ex2_approx(m_s[w * 8 + gg] - M);
+        L = fmaf(f, l_s[w * 8 + gg], L);
+        O = fmaf(f, mrg[(w * G + gg) * D + dd], O);
+      }
+      p.ws_o[(slot * G + gg) * D + dd] = O;
+      if (dd == 0) *reinterpret_cast<float2*>(&p.ws_ml[(slot * G + gg) * 2]) = make_float2(M, L);
+    }
+    // After an expired wait every warp has still passed the same barriers; all
+    // stop here together.
+    if (threadIdx.x == 0) *stop_flag = *abort_flag;
+    named_bar_sync(1, C::NWARP * 32);
+    if (*stop_flag) break;
+  }
+}
+
+// One warp per (sequence, query head): the partial results of its stretch of
+// the list, joined.
 template <int D>
 __global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const __grid_constant__ Kv4DecodeParams p) {
   constexpr int E = D / 32;
   const int row = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   if (row >= p.B * p.Hq) return;
   const int G = p.Hq / p.Hkv;
-  const int b = row / p.Hq, h = row % p.Hq;
-  const size_t s0 = ((size_t)b * p.Hkv + h / G) * p.nsplit;
+  const int b = row / p.Hq, hkv = row % p.Hq / G, gq = row % G;
+  const long long total = (long long)p.ws_prefix[p.B] * p.Hkv;
+  const int count = p.ws_prefix[b + 1] - p.ws_prefix[b];
+  const int n_cta = (int)min((long long)p.n_cta, total);
+  __nv_bfloat16* dst = p.o + (size_t)row * D + lane * E;
   float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int c = 0; c < p.nsplit; ++c) M = fmaxf(M, p.ws_ml[((s0 + c) * G + h % G) * 2]);
-  for (int c = 0; c < p.nsplit; ++c) {
-    const size_t at = (s0 + c) * G + h % G;
-    const float m = p.ws_ml[at * 2];
-    const float f = m == -INFINITY ? 0.f : ex2_approx(m - M);
-    L = fmaf(f, p.ws_ml[at * 2 + 1], L);
+  if (count > 0) {
+    const long long first = (long long)p.ws_prefix[b] * p.Hkv + (long long)hkv * count;
+    // block i of tile t: the last with total * i / n <= t
+    const int c0 = (int)(((first + 1) * n_cta - 1) / total), c1 = (int)(((first + count) * n_cta - 1) / total);
+    const size_t s0 = (size_t)b * p.Hkv + hkv;
+    for (int c = c0; c <= c1; ++c) M = fmaxf(M, p.ws_ml[((s0 + c) * G + gq) * 2]);
+    for (int c = c0; c <= c1; ++c) {
+      const size_t at = (s0 + c) * G + gq;
+      const float m = p.ws_ml[at * 2];
+      const float f = m == -INFINITY ? 0.f : ex2_approx(m - M);
+      L = fmaf(f, p.ws_ml[at * 2 + 1], L);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(f, p.ws_o[at * D + lane * E + e], o[e]);
+      for (int e = 0; e < E; ++e) o[e] = fmaf(f, p.ws_o[at * D + lane * E + e], o[e]);
+    }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  __nv_bfloat16* dst = p.o + (size_t)row * D + lane * E;
 #pragma unroll
   for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
   if (lane == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
