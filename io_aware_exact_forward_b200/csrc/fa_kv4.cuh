@@ -259,13 +259,22 @@ __device__ __forceinline__ void ldsm_x2_t(uint32_t addr, uint32_t& r0, uint32_t&
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t r;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr));
   return r;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 r;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
   return r;
+}
+// D = A B + C with C apart from D, so that a constant C stays in its registers.
+__device__ __forceinline__ void mma_16816_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // The steps of one row's params, as words of two.
@@ -401,7 +410,8 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
   const int g = lane >> 2, t4 = lane & 3;
   const int kw = warp * 16;  // this warp's 16 keys of every tile
   bool ok = true;
-  int t = 0;
+  int s = 0;            // stage, and the parity of its use
+  uint32_t phase = 0;
   for (long long at = t_begin; at < t_end;) {
     const Kv4Segment sg(pre, p.B, p.Hkv, at, t_end);
     const Kv4Seq sq(p, p.seqlens[sg.b]);
@@ -409,7 +419,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
 
     // Q as the row operand: row g, dims of group c in the order the codes have
     uint32_t qa[NG][4];
-    float qinit[NG];      // -136 sum of the group's q
+    float qinit[NG][2];   // -136 sum of the group's q, twice: the accumulator's two columns
     uint32_t za0, za2 = 0u;
     {
       const __nv_bfloat16* qrow = p.q + ((size_t)sg.b * p.Hq + sg.hkv * G + (g < G ? g : 0)) * D;
@@ -427,7 +437,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
         q8 += __shfl_xor_sync(0xffffffffu, q8, 1);
         q8 += __shfl_xor_sync(0xffffffffu, q8, 2);
         qs[c] = q8;
-        qinit[c] = -136.f * q8;
+        qinit[c][0] = qinit[c][1] = -136.f * q8;
       }
       // sum q of every group in three bf16 parts: columns (part, group) of the
       // row operand that meets the centres
@@ -461,9 +471,8 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) oacc[c][k][e] = 0.f;
 
-    for (int j = 0; j < sg.n; ++j, ++t) {
-      const int s = t % C::NSTAGE;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_full(s), (t / C::NSTAGE) & 1, wc));
+    for (int j = 0; j < sg.n; ++j) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_full(s), phase, wc));
       if (ok) {
         const uint32_t st = sbase + s * C::STAGE_BYTES;
         const int key0 = sq.tile(sg.first + j) * C::TILE;
@@ -500,18 +509,22 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
           uint32_t s0[NG / 2], s1[NG / 2];
           kv4_steps<NG>(kp + (2 * t4) * C::PB, s0);
           kv4_steps<NG>(kp + (2 * t4 + 1) * C::PB, s1);
-          float sz[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_16816(sz, za0, 0u, za2, 0u, zw, zw);
+          float sz[4];
+          mma_16816_c(sz, za0, 0u, za2, 0u, zw, zw, 0.f, 0.f, 0.f, 0.f);
           float2 tot = make_float2(sz[0], sz[1]);
+          // two groups per accumulator: the even one's rows are 0..7, the odd
+          // one's 8..15
 #pragma unroll
-          for (int c = 0; c < NG; ++c) {
-            float a[4] = {qinit[c], qinit[c], 0.f, 0.f};
-            const uint32_t w = kc[nb][c];
-            mma_16816(a, qa[c][0], 0u, qa[c][1], 0u, kv4_pair(w, 0), kv4_pair(w, 1));
-            mma_16816(a, qa[c][2], 0u, qa[c][3], 0u, kv4_pair(w, 2), kv4_pair(w, 3));
-            const float2 ss = (c & 1) ? make_float2(bf16_hi(s0[c / 2]), bf16_hi(s1[c / 2]))
-                                      : make_float2(bf16_lo(s0[c / 2]), bf16_lo(s1[c / 2]));
-            tot = __ffma2_rn(ss, make_float2(a[0], a[1]), tot);
+          for (int c = 0; c < NG; c += 2) {
+            float a[4];
+            const uint32_t w0 = kc[nb][c], w1 = kc[nb][c + 1];
+            mma_16816_c(a, qa[c][0], 0u, qa[c][1], 0u, kv4_pair(w0, 0), kv4_pair(w0, 1), qinit[c][0], qinit[c][1],
+                        qinit[c + 1][0], qinit[c + 1][1]);
+            mma_16816(a, qa[c][2], 0u, qa[c][3], 0u, kv4_pair(w0, 2), kv4_pair(w0, 3));
+            mma_16816(a, 0u, qa[c + 1][0], 0u, qa[c + 1][1], kv4_pair(w1, 0), kv4_pair(w1, 1));
+            mma_16816(a, 0u, qa[c + 1][2], 0u, qa[c + 1][3], kv4_pair(w1, 2), kv4_pair(w1, 3));
+            tot = __ffma2_rn(make_float2(bf16_lo(s0[c / 2]), bf16_lo(s1[c / 2])), make_float2(a[0], a[1]), tot);
+            tot = __ffma2_rn(make_float2(bf16_hi(s0[c / 2]), bf16_hi(s1[c / 2])), make_float2(a[2], a[3]), tot);
           }
           sc[2 * nb] = tot.x * p.scale_log2;
           sc[2 * nb + 1] = tot.y * p.scale_log2;
@@ -593,6 +606,10 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_empty(s));
+      if (++s == C::NSTAGE) {
+        s = 0;
+        phase ^= 1;
+      }
     }
 
     // ---- the four warps' results, joined
