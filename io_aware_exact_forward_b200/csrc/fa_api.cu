@@ -1212,14 +1212,14 @@ extern "C" int fa_kv4_read(void* k, void* v, const void* k_codes, const void* k_
 
 namespace fa {
 
-// Codes as [pairs][Tk][d/2] bytes with box {d/2, 64, 1}, in the swizzle of
+// Codes as [pairs][Tk][d/2] bytes with box {d/2, 32, 1}, in the swizzle of
 // their row width.
 static int kv4_tmap(CUtensorMap* m, const void* base, uint64_t pairs, uint64_t Tk, int d) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return FA_ERR_CUDA;
   const cuuint64_t dims[3] = {(cuuint64_t)d / 2, Tk, pairs};
   const cuuint64_t strides[2] = {(cuuint64_t)d / 2, Tk * (d / 2)};
-  const cuuint32_t box[3] = {(cuuint32_t)d / 2, 64, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)d / 2, 32, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,

@@ -169,16 +169,19 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
 // operand wants, so V^T enters as the row operand, 16 dims by 16 keys, and P^T
 // as the column operand: both come out of the score's accumulator in place.
 //
-// Work.  A persistent grid; every sequence's visible 64-key tiles, in the order
+// Work.  A persistent grid; every sequence's visible 128-key tiles, in the order
 // of (sequence, KV head), are one long list that the blocks share out evenly
 // whatever the lengths are.  A block's stretch of one (sequence, KV head) ends
 // in a partial result (slot: block + pair, both grow along the list), and a
-// second kernel joins them.
+// second kernel joins them.  Each warp of a block takes 32 keys of every tile
+// through a ring of its own, which it fills itself: no warp waits for another
+// before a stretch ends, and none is spent on loading, so that 16 warps of 128
+// registers compute on an SM.
 static constexpr int kKv4MaxSeqs = 1024;  // sequences per launch
-static constexpr int kKv4MaxGrid = 512;
+static constexpr int kKv4MaxGrid = 1024;
 
 struct Kv4DecodeParams {
-  CUtensorMap tm_k;        // codes [B * Hkv][Tk_max][d/2] bytes, box {d/2, 64, 1}, swizzled
+  CUtensorMap tm_k;        // codes [B * Hkv][Tk_max][d/2] bytes, box {d/2, 32, 1}, swizzled
   CUtensorMap tm_v;
   const __nv_bfloat16* q;  // [B][Hq][d]
   const __nv_bfloat16* k_params;  // [B][Hkv][Tk_max][2 d/32]
@@ -203,9 +206,9 @@ struct Kv4Seq {
   __device__ __forceinline__ Kv4Seq(const Kv4DecodeParams& p, int seqlen) {
     len = min(max(seqlen, 0), p.Tk_max);
     lo = p.window > 0 ? max(0, len - p.window) : 0;
-    const int end = (len + 63) >> 6;
-    n_sink = min(end, (p.sinks + 63) >> 6);
-    lo_tile = max(n_sink, lo >> 6);
+    const int end = (len + 127) >> 7;
+    n_sink = min(end, (p.sinks + 127) >> 7);
+    lo_tile = max(n_sink, lo >> 7);
     count = n_sink + max(0, end - lo_tile);
   }
   __device__ __forceinline__ int tile(int j) const { return j < n_sink ? j : lo_tile + j - n_sink; }
@@ -213,23 +216,26 @@ struct Kv4Seq {
 
 template <int D, int G>
 struct Kv4Cfg {
-  static constexpr int TILE = 64;                     // keys per stage
-  static constexpr int NWARP = 4;                     // compute warps, 16 keys each
-  static constexpr int THREADS = (NWARP + 1) * 32;
+  static constexpr int SLICE = 32;                    // keys of a warp's stage
+  static constexpr int NWARP = 4;
+  static constexpr int TILE = NWARP * SLICE;
+  static constexpr int THREADS = NWARP * 32;
   static constexpr int CB = D / 2, NG = D / kKv4Group, PB = 4 * NG;  // bytes of a row's codes, groups, bytes of params
-  static constexpr int OFF_K = 0, OFF_V = TILE * CB, OFF_KP = 2 * TILE * CB, OFF_VP = OFF_KP + TILE * PB;
-  static constexpr int STAGE_BYTES = OFF_VP + TILE * PB;
-  static constexpr int NSTAGE = (D == 128) ? 5 : 10;
-  static constexpr int OFF_MRG = NSTAGE * STAGE_BYTES;           // [NWARP][G][D] fp32
-  static constexpr int OFF_ML = OFF_MRG + NWARP * G * D * 4;     // m, l: [NWARP][8] each
+  static constexpr int OFF_K = 0, OFF_V = SLICE * CB, OFF_KP = 2 * SLICE * CB, OFF_VP = OFF_KP + SLICE * PB;
+  static constexpr int STAGE_BYTES = OFF_VP + SLICE * PB;
+  static constexpr int NSTAGE = (D == 128) ? 2 : 4;              // per warp
+  static constexpr int OFF_MRG = NWARP * NSTAGE * STAGE_BYTES;   // [NWARP][G][D / 2] fp32: half the dims at a time
+  static constexpr int OFF_ML = OFF_MRG + NWARP * G * D * 2;     // m, l: [NWARP][8] each
   static constexpr int OFF_PRE = OFF_ML + 2 * NWARP * 8 * 4;     // prefix [kKv4MaxSeqs + 1]
   static constexpr int OFF_SCAN = OFF_PRE + (kKv4MaxSeqs + 4) * 4;
-  static constexpr int OFF_BAR = OFF_SCAN + 64;
-  static constexpr int OFF_FLAG = OFF_BAR + 2 * NSTAGE * 8;
+  static constexpr int OFF_BAR = OFF_SCAN + 64;                  // full [NWARP][NSTAGE]
+  static constexpr int OFF_FLAG = OFF_BAR + NWARP * NSTAGE * 8;
   static constexpr int SMEM_BYTES = OFF_FLAG + 16 + 1024;        // + alignment slack
-  static constexpr int CTAS = 3;                                 // per SM
+  static constexpr int CTAS = 4;                                 // per SM
   static constexpr float RESCALE_THRESHOLD = 8.0f;
-  static_assert(STAGE_BYTES % 1024 == 0 && OFF_V % 1024 == 0, "swizzled tiles need their alignment");
+  // the 64-byte swizzle repeats every 512 bytes, the 32-byte one every 256
+  static_assert(STAGE_BYTES % 512 == 0 && OFF_V % 512 == 0, "swizzled tiles need their alignment");
+  static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "shared memory of an SM");
 };
 
 // Byte offset of 16-byte chunk c of row r of a code tile (the 64-byte swizzle
@@ -289,22 +295,31 @@ __device__ __forceinline__ void kv4_steps(uint32_t addr, uint32_t (&w)[NG / 2]) 
   }
 }
 
-// One stretch of the tile list within one (sequence, KV head).
-struct Kv4Segment {
-  int b, hkv, first, n;  // sequence, KV head, first visible tile (index), tiles
-  __device__ __forceinline__ Kv4Segment(const int* pre, int B, int Hkv, long long at, long long end) {
+// One stretch of the tile list within one (sequence, KV head), as one warp
+// walks it: its slice of the stretch's j-th tile starts at key(j).
+struct Kv4Stretch {
+  int n, pair;             // tiles; (sequence, KV head) within this launch
+  int len, lo;             // the sequence's keys, and the first in its window
+  int n_sink, key_a, key_b;
+  __device__ __forceinline__ Kv4Stretch(const Kv4DecodeParams& p, const int* pre, int at, int left, int tile,
+                                        int slice_off) {
     // the sequence whose tiles hold `at`: the last b with pre[b] * Hkv <= at
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((long long)pre[mid] * Hkv <= at) lo = mid; else hi = mid - 1;
+    int b = 0, hi = p.B - 1;
+    while (b < hi) {
+      const int mid = (b + hi + 1) >> 1;
+      if (pre[mid] * p.Hkv <= at) b = mid; else hi = mid - 1;
     }
-    b = lo;
     const int count = pre[b + 1] - pre[b];
-    const int off = (int)(at - (long long)pre[b] * Hkv);
-    hkv = off / count;
-    first = off - hkv * count;
-    n = (int)min((long long)(count - first), end - at);
+    const int off = at - pre[b] * p.Hkv;
+    const int hkv = off / count, first = off - hkv * count;
+    const Kv4Seq sq(p, p.seqlens[b]);
+    n = min(count - first, left);
+    pair = b * p.Hkv + hkv;
+    len = sq.len;
+    lo = sq.lo;
+    n_sink = sq.n_sink - first;
+    key_a = first * tile + slice_off;
+    key_b = (sq.lo_tile - sq.n_sink + first) * tile + slice_off;
   }
 };
 
@@ -323,24 +338,22 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
   int* scan = reinterpret_cast<int*>(smem + C::OFF_SCAN);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);
   volatile int* stop_flag = abort_flag + 1;
-  auto bar_full = [&](int s) { return sbase + C::OFF_BAR + 8u * s; };
-  auto bar_empty = [&](int s) { return sbase + C::OFF_BAR + 8u * (C::NSTAGE + s); };
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  // this warp's barriers and ring
+  auto bar_full = [&](int s) { return sbase + C::OFF_BAR + 8u * (warp * C::NSTAGE + s); };
+  const uint32_t ring_off = warp * C::NSTAGE * C::STAGE_BYTES;
   WaitCtl wc{abort_flag, p.wait_limit_ns};
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     *stop_flag = 0;
-    for (int s = 0; s < C::NSTAGE; ++s) {
-      mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), C::NWARP);
-    }
+    for (int s = 0; s < C::NWARP * C::NSTAGE; ++s) mbar_init(sbase + C::OFF_BAR + 8u * s, 1);
     fence_barrier_init();
   }
   // ---- prefix sum of the sequences' visible tiles, the same in every block
   {
-    constexpr int PER = (kKv4MaxSeqs + C::THREADS - 1) / C::THREADS;
+    constexpr int PER = kKv4MaxSeqs / C::THREADS + 1;  // up to and with the total at index B
     const int i0 = threadIdx.x * PER;
     int cnt[PER], sum = 0;
 #pragma unroll
@@ -368,61 +381,52 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
     }
   }
   __syncthreads();
-  const long long total = (long long)pre[p.B] * p.Hkv;
-  const int n_cta = (int)min((long long)p.n_cta, total);
+  const int total = pre[p.B] * p.Hkv;  // at most 2^30, checked on the host
+  const int n_cta = min(p.n_cta, total);
   if ((int)blockIdx.x >= n_cta) return;
-  const long long t_begin = total * blockIdx.x / n_cta, t_end = total * (blockIdx.x + 1) / n_cta;
+  int at = (int)((long long)total * blockIdx.x / n_cta);
+  int left = (int)((long long)total * (blockIdx.x + 1) / n_cta) - at;
 
-  if (warp == C::NWARP) {
-    // ---------------------------------------------------------- producer
-    if (lane == 0) {
-      tma_prefetch_desc(&p.tm_k);
-      tma_prefetch_desc(&p.tm_v);
-      bool ok = true;
-      int t = 0;
-      for (long long at = t_begin; at < t_end && ok;) {
-        const Kv4Segment sg(pre, p.B, p.Hkv, at, t_end);
-        const Kv4Seq sq(p, p.seqlens[sg.b]);
-        const int pair = p.pair0 + sg.b * p.Hkv + sg.hkv;
-        for (int j = 0; j < sg.n; ++j, ++t) {
-          const int s = t % C::NSTAGE;
-          const int k0 = sq.tile(sg.first + j) * C::TILE;
-          if (t >= C::NSTAGE) ok = mbar_wait(bar_empty(s), (t / C::NSTAGE - 1) & 1, wc);
-          if (!ok) break;
-          const uint32_t st = sbase + s * C::STAGE_BYTES;
-          const size_t row = (size_t)pair * p.Tk_max + k0;
-          mbar_arrive_expect_tx(bar_full(s), C::STAGE_BYTES);
-          tma_load_3d(st + C::OFF_K, &p.tm_k, bar_full(s), 0, k0, pair);
-          bulk_load(st + C::OFF_KP, p.k_params + row * 2 * NG, C::TILE * C::PB, bar_full(s));
-          tma_load_3d(st + C::OFF_V, &p.tm_v, bar_full(s), 0, k0, pair);
-          bulk_load(st + C::OFF_VP, p.v_params + row * 2 * NG, C::TILE * C::PB, bar_full(s));
-        }
-        at += sg.n;
-      }
-      if (!ok)  // every copy already issued lands before the block can exit
-        for (int k = max(0, t - C::NSTAGE); k < t; ++k)
-          mbar_wait_drain(bar_full(k % C::NSTAGE), (k / C::NSTAGE) & 1, p.wait_limit_ns);
-    }
-    return;  // no named barrier below
-  }
-
-  // ------------------------------------------------------------ compute
   const int g = lane >> 2, t4 = lane & 3;
-  const int kw = warp * 16;  // this warp's 16 keys of every tile
   bool ok = true;
-  int s = 0;            // stage, and the parity of its use
-  uint32_t phase = 0;
-  for (long long at = t_begin; at < t_end;) {
-    const Kv4Segment sg(pre, p.B, p.Hkv, at, t_end);
-    const Kv4Seq sq(p, p.seqlens[sg.b]);
-    at += sg.n;
+  uint32_t phases = 0;  // bit s: parity of the next use of stage s
 
+  auto key_of = [&](const Kv4Stretch& sg, int j) { return (j < sg.n_sink ? sg.key_a : sg.key_b) + j * C::TILE; };
+  auto needed = [&](const Kv4Stretch& sg, int ks) {
+    return ks < sg.len && (ks + C::SLICE > sg.lo || ks < p.sinks);
+  };
+  auto load = [&](const Kv4Stretch& sg, int j) {
+    const int ks = key_of(sg, j);
+    if (lane == 0 && j < sg.n && needed(sg, ks)) {
+      const int s = j % C::NSTAGE;
+      const int pair = p.pair0 + sg.pair;
+      const uint32_t st = sbase + ring_off + s * C::STAGE_BYTES;
+      const size_t row = (size_t)pair * p.Tk_max + ks;
+      mbar_arrive_expect_tx(bar_full(s), C::STAGE_BYTES);
+      tma_load_3d(st + C::OFF_K, &p.tm_k, bar_full(s), 0, ks, pair);
+      bulk_load(st + C::OFF_KP, p.k_params + row * 2 * NG, C::SLICE * C::PB, bar_full(s));
+      tma_load_3d(st + C::OFF_V, &p.tm_v, bar_full(s), 0, ks, pair);
+      bulk_load(st + C::OFF_VP, p.v_params + row * 2 * NG, C::SLICE * C::PB, bar_full(s));
+    }
+  };
+
+  if (lane == 0) {
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  Kv4Stretch sg(p, pre, at, left, C::TILE, warp * C::SLICE);
+#pragma unroll
+  for (int j = 0; j < C::NSTAGE; ++j) load(sg, j);
+
+  while (true) {
+    at += sg.n;
+    left -= sg.n;
     // Q as the row operand: row g, dims of group c in the order the codes have
     uint32_t qa[NG][4];
     float qinit[NG][2];   // -136 sum of the group's q, twice: the accumulator's two columns
     uint32_t za0, za2 = 0u;
     {
-      const __nv_bfloat16* qrow = p.q + ((size_t)sg.b * p.Hq + sg.hkv * G + (g < G ? g : 0)) * D;
+      const __nv_bfloat16* qrow = p.q + ((size_t)sg.pair * G + (g < G ? g : 0)) * D;
       float qs[NG];
 #pragma unroll
       for (int c = 0; c < NG; ++c) {
@@ -472,23 +476,33 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
         for (int e = 0; e < 4; ++e) oacc[c][k][e] = 0.f;
 
     for (int j = 0; j < sg.n; ++j) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_full(s), phase, wc));
-      if (ok) {
-        const uint32_t st = sbase + s * C::STAGE_BYTES;
-        const int key0 = sq.tile(sg.first + j) * C::TILE;
-        const bool whole = key0 + C::TILE <= sq.len && (key0 >= sq.lo || key0 + C::TILE <= p.sinks);
-        auto visible = [&](int key) { return key < sq.len && (key >= sq.lo || key < p.sinks); };
-        if (!whole) {
-          // A masked key's p is 0, but 0 times what an unwritten row's params
-          // may hold (NaN, infinity) is not: zero them.
-          if (lane < 16 && !visible(key0 + kw + lane)) {
-            uint32_t* row = reinterpret_cast<uint32_t*>(smem + s * C::STAGE_BYTES + C::OFF_VP + (kw + lane) * C::PB);
+      const int s = j % C::NSTAGE;
+      const int ks = key_of(sg, j);
+      if (!needed(sg, ks)) {
+        load(sg, j + C::NSTAGE);
+        continue;
+      }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_full(s), (phases >> s) & 1u, wc));
+      if (!ok) break;
+      phases ^= 1u << s;
+      const bool whole = ks + C::SLICE <= sg.len && (ks >= sg.lo || ks + C::SLICE <= p.sinks);
+      auto visible = [&](int key) { return key < sg.len && (key >= sg.lo || key < p.sinks); };
+      if (!whole) {
+        // A masked key's p is 0, but 0 times what an unwritten row's params
+        // may hold (NaN, infinity) is not: zero them.
+        if (!visible(ks + lane)) {
+          uint32_t* row =
+              reinterpret_cast<uint32_t*>(smem + ring_off + s * C::STAGE_BYTES + C::OFF_VP + lane * C::PB);
 #pragma unroll
-            for (int i = 0; i < C::PB / 4; ++i) row[i] = 0u;
-          }
-          fence_proxy_async_smem();  // before the next bulk load into this stage
-          __syncwarp();
+          for (int i = 0; i < C::PB / 4; ++i) row[i] = 0u;
         }
+        fence_proxy_async_smem();  // before the next bulk load into this stage
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int u = 0; u < C::SLICE / 16; ++u) {  // 16 keys at a time
+        const uint32_t st = sbase + ring_off + s * C::STAGE_BYTES;
+        const int kw = 16 * u, key0 = ks;
 
         // ---- scores of row g against keys kw + 8 nb + 2t (+1)
         uint32_t kc[2][NG];
@@ -604,13 +618,18 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_empty(s));
-      if (++s == C::NSTAGE) {
-        s = 0;
-        phase ^= 1;
-      }
+      __syncwarp();  // the stage has been read
+      load(sg, j + C::NSTAGE);
     }
+
+    // the next stretch's first loads fly while this one's results are joined
+    const size_t slot = (size_t)blockIdx.x + sg.pair;
+    if (left > 0 && ok) {
+      sg = Kv4Stretch(p, pre, at, left, C::TILE, warp * C::SLICE);
+#pragma unroll
+      for (int j = 0; j < C::NSTAGE; ++j) load(sg, j);
+    }
+    const bool more = left > 0;
 
     // ---- the four warps' results, joined
     float l_row = l_part + __shfl_xor_sync(0xffffffffu, l_part, 1);
@@ -620,38 +639,45 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
       l_s[warp * 8 + g] = l_row;
     }
 #pragma unroll
-    for (int c = 0; c < NG; ++c) {
-      const int zrow = NG == 4 ? 4 + c : c;
-      const float add0 = __shfl_sync(0xffffffffu, zacc[0], 4 * zrow + t4);
-      const float add1 = __shfl_sync(0xffffffffu, zacc[1], 4 * zrow + t4);
-      if (2 * t4 < G)
-        *reinterpret_cast<float4*>(&mrg[(warp * G + 2 * t4) * D + 32 * c + 4 * g]) =
-            make_float4(oacc[c][0][0] + add0, oacc[c][0][2] + add0, oacc[c][1][0] + add0, oacc[c][1][2] + add0);
-      if (2 * t4 + 1 < G)
-        *reinterpret_cast<float4*>(&mrg[(warp * G + 2 * t4 + 1) * D + 32 * c + 4 * g]) =
-            make_float4(oacc[c][0][1] + add1, oacc[c][0][3] + add1, oacc[c][1][1] + add1, oacc[c][1][3] + add1);
-    }
-    named_bar_sync(1, C::NWARP * 32);
-    const size_t slot = (size_t)blockIdx.x + sg.b * p.Hkv + sg.hkv;
-    for (int idx = threadIdx.x; idx < G * D; idx += C::NWARP * 32) {
-      const int gg = idx / D, dd = idx % D;
-      float M = -INFINITY, L = 0.f, O = 0.f;
+    for (int h = 0; h < 2; ++h) {  // half of the dims at a time
 #pragma unroll
-      for (int w = 0; w < C::NWARP; ++w) M = fmaxf(M, m_s[w * 8 + gg]);
-#pragma unroll
-      for (int w = 0; w < C::NWARP; ++w) {
-        const float f = m_s[w * 8 + gg] == -INFINITY ? 0.f : ex2_approx(m_s[w * 8 + gg] - M);
-        L = fmaf(f, l_s[w * 8 + gg], L);
-        O = fmaf(f, mrg[(w * G + gg) * D + dd], O);
+      for (int c = h * (NG / 2); c < (h + 1) * (NG / 2); ++c) {
+        const int zrow = NG == 4 ? 4 + c : c;
+        const float add0 = __shfl_sync(0xffffffffu, zacc[0], 4 * zrow + t4);
+        const float add1 = __shfl_sync(0xffffffffu, zacc[1], 4 * zrow + t4);
+        const int at_d = 32 * c - h * (D / 2) + 4 * g;
+        if (2 * t4 < G)
+          *reinterpret_cast<float4*>(&mrg[(warp * G + 2 * t4) * (D / 2) + at_d]) =
+              make_float4(oacc[c][0][0] + add0, oacc[c][0][2] + add0, oacc[c][1][0] + add0, oacc[c][1][2] + add0);
+        if (2 * t4 + 1 < G)
+          *reinterpret_cast<float4*>(&mrg[(warp * G + 2 * t4 + 1) * (D / 2) + at_d]) =
+              make_float4(oacc[c][0][1] + add1, oacc[c][0][3] + add1, oacc[c][1][1] + add1, oacc[c][1][3] + add1);
       }
-      p.ws_o[(slot * G + gg) * D + dd] = O;
-      if (dd == 0) *reinterpret_cast<float2*>(&p.ws_ml[(slot * G + gg) * 2]) = make_float2(M, L);
+      __syncthreads();
+      for (int idx = threadIdx.x; idx < G * (D / 2); idx += C::THREADS) {
+        const int gg = idx / (D / 2), dd = idx % (D / 2);
+        float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+        for (int w = 0; w < C::NWARP; ++w) M = fmaxf(M, m_s[w * 8 + gg]);
+#pragma unroll
+        for (int w = 0; w < C::NWARP; ++w) {
+          const float f = m_s[w * 8 + gg] == -INFINITY ? 0.f : ex2_approx(m_s[w * 8 + gg] - M);
+          L = fmaf(f, l_s[w * 8 + gg], L);
+          O = fmaf(f, mrg[(w * G + gg) * (D / 2) + dd], O);
+        }
+        p.ws_o[(slot * G + gg) * D + h * (D / 2) + dd] = O;
+        if (h == 0 && dd == 0) *reinterpret_cast<float2*>(&p.ws_ml[(slot * G + gg) * 2]) = make_float2(M, L);
+      }
+      // After an expired wait every warp still passes the same barriers; all
+      // stop together.
+      if (h == 1 && threadIdx.x == 0) *stop_flag = *abort_flag;
+      __syncthreads();
     }
-    // After an expired wait every warp has still passed the same barriers; all
-    // stop here together.
-    if (threadIdx.x == 0) *stop_flag = *abort_flag;
-    named_bar_sync(1, C::NWARP * 32);
-    if (*stop_flag) break;
+    if (!more || *stop_flag) break;
+  }
+  if (*stop_flag && lane == 0) {
+    // after an expired wait: every copy this warp issued lands before the block's memory goes
+    for (int s = 0; s < C::NSTAGE; ++s) mbar_wait_drain(bar_full(s), (phases >> s) & 1u, p.wait_limit_ns);
   }
 }
 
