@@ -246,16 +246,29 @@ __device__ __forceinline__ uint32_t kv4_swz(int r, int c) {
   return (uint32_t)(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
 }
 
-// Nibble k of both halves as the bf16 pair 128 + u.
-__device__ __forceinline__ uint32_t kv4_pair(uint32_t w, int k) { return ((w >> (4 * k)) & 0x000F000Fu) | 0x43004300u; }
-
-// The same as u - 8.
-__device__ __forceinline__ uint32_t kv4_pair_c(uint32_t w, int k) {
-  const uint32_t u = kv4_pair(w, k), m136 = 0x43084308u;
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&m136));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
+// The two constants of the conversions, in registers that the compiler cannot
+// see through: as literals, the mask and the OR are two instructions (an
+// instruction takes one literal), not one.
+struct Kv4Const {
+  uint32_t magic, m136;  // bf16 pairs (128, 128) and (136, 136)
+  __device__ __forceinline__ Kv4Const() {
+    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(magic));
+    asm volatile("mov.b32 %0, 0x43084308;" : "=r"(m136));
+  }
+  // Nibble k of both halves as the bf16 pair 128 + u.
+  __device__ __forceinline__ uint32_t pair(uint32_t w, int k) const {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(r) : "r"(w >> (4 * k)), "r"(magic));
+    return r;
+  }
+  // The same as u - 8.
+  __device__ __forceinline__ uint32_t pair_c(uint32_t w, int k) const {
+    const uint32_t u = pair(w, k);
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&m136));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+};
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -388,6 +401,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
   int left = (int)((long long)total * (blockIdx.x + 1) / n_cta) - at;
 
   const int g = lane >> 2, t4 = lane & 3;
+  const Kv4Const kc4;
   bool ok = true;
   uint32_t phases = 0;  // bit s: parity of the next use of stage s
 
@@ -532,11 +546,11 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
           for (int c = 0; c < NG; c += 2) {
             float a[4];
             const uint32_t w0 = kc[nb][c], w1 = kc[nb][c + 1];
-            mma_16816_c(a, qa[c][0], 0u, qa[c][1], 0u, kv4_pair(w0, 0), kv4_pair(w0, 1), qinit[c][0], qinit[c][1],
+            mma_16816_c(a, qa[c][0], 0u, qa[c][1], 0u, kc4.pair(w0, 0), kc4.pair(w0, 1), qinit[c][0], qinit[c][1],
                         qinit[c + 1][0], qinit[c + 1][1]);
-            mma_16816(a, qa[c][2], 0u, qa[c][3], 0u, kv4_pair(w0, 2), kv4_pair(w0, 3));
-            mma_16816(a, 0u, qa[c + 1][0], 0u, qa[c + 1][1], kv4_pair(w1, 0), kv4_pair(w1, 1));
-            mma_16816(a, 0u, qa[c + 1][2], 0u, qa[c + 1][3], kv4_pair(w1, 2), kv4_pair(w1, 3));
+            mma_16816(a, qa[c][2], 0u, qa[c][3], 0u, kc4.pair(w0, 2), kc4.pair(w0, 3));
+            mma_16816(a, 0u, qa[c + 1][0], 0u, qa[c + 1][1], kc4.pair(w1, 0), kc4.pair(w1, 1));
+            mma_16816(a, 0u, qa[c + 1][2], 0u, qa[c + 1][3], kc4.pair(w1, 2), kc4.pair(w1, 3));
             tot = __ffma2_rn(make_float2(bf16_lo(s0[c / 2]), bf16_lo(s1[c / 2])), make_float2(a[0], a[1]), tot);
             tot = __ffma2_rn(make_float2(bf16_hi(s0[c / 2]), bf16_hi(s1[c / 2])), make_float2(a[2], a[3]), tot);
           }
@@ -613,8 +627,8 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
             const uint32_t b0 = pack_bf16x2(ps[0], ps[1]), b1 = pack_bf16x2(ps[2], ps[3]);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-              mma_16816(oacc[c][k], kv4_pair_c(vc[cc][0], 2 * k), kv4_pair_c(vc[cc][0], 2 * k + 1),
-                        kv4_pair_c(vc[cc][1], 2 * k), kv4_pair_c(vc[cc][1], 2 * k + 1), b0, b1);
+              mma_16816(oacc[c][k], kc4.pair_c(vc[cc][0], 2 * k), kc4.pair_c(vc[cc][0], 2 * k + 1),
+                        kc4.pair_c(vc[cc][1], 2 * k), kc4.pair_c(vc[cc][1], 2 * k + 1), b0, b1);
           }
         }
       }
