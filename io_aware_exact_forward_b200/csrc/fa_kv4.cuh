@@ -273,9 +273,6 @@ struct Kv4Const {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-__device__ __forceinline__ void ldsm_x2_t(uint32_t addr, uint32_t& r0, uint32_t& r1) {
-  asm volatile("ldmatrix.sync.aligned.x2.trans.m8n8.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
-}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t r;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr));
@@ -436,6 +433,9 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
     at += sg.n;
     left -= sg.n;
     // Q as the row operand: row g, dims of group c in the order the codes have
+    // (an operand's four registers are neighbours: rows 8..15, which no query
+    // has, hold the next group's Q rather than zeros, so that every operand is
+    // four registers that stay)
     uint32_t qa[NG][4];
     float qinit[NG][2];   // -136 sum of the group's q, twice: the accumulator's two columns
     uint32_t za0, za2 = 0u;
@@ -513,118 +513,129 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
         fence_proxy_async_smem();  // before the next bulk load into this stage
         __syncwarp();
       }
-#pragma unroll 1
-      for (int u = 0; u < C::SLICE / 16; ++u) {  // 16 keys at a time
-        const uint32_t st = sbase + ring_off + s * C::STAGE_BYTES;
-        const int kw = 16 * u, key0 = ks;
+      const uint32_t st = sbase + ring_off + s * C::STAGE_BYTES;
 
-        // ---- scores of row g against keys kw + 8 nb + 2t (+1)
+      // ---- scores of row g against keys ks + 16 u + 8 nb + 2t (+1)
+      float2 sc[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
         uint32_t kc[2][NG];
         if constexpr (D == 128) {
 #pragma unroll
           for (int nb = 0; nb < 2; ++nb)
-            ldsm_x4(st + C::OFF_K + kv4_swz<D>(kw + 8 * nb + (lane & 7), lane >> 3), kc[nb][0], kc[nb][1], kc[nb][2],
-                    kc[nb][3]);
+            ldsm_x4(st + C::OFF_K + kv4_swz<D>(16 * u + 8 * nb + (lane & 7), lane >> 3), kc[nb][0], kc[nb][1],
+                    kc[nb][2], kc[nb][3]);
         } else {
-          ldsm_x4(st + C::OFF_K + kv4_swz<D>(kw + ((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1), kc[0][0],
+          ldsm_x4(st + C::OFF_K + kv4_swz<D>(16 * u + ((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1), kc[0][0],
                   kc[0][1], kc[1][0], kc[1][1]);
         }
-        float sc[4];
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb) {
-          const uint32_t kp = st + C::OFF_KP + (kw + 8 * nb) * C::PB;
+          const uint32_t kp = st + C::OFF_KP + (16 * u + 8 * nb) * C::PB;
           const uint32_t zw = lds32(kp + g * C::PB + 2 * NG + (NG == 4 ? 4 * (t4 & 1) : 0));
           uint32_t s0[NG / 2], s1[NG / 2];
           kv4_steps<NG>(kp + (2 * t4) * C::PB, s0);
           kv4_steps<NG>(kp + (2 * t4 + 1) * C::PB, s1);
           float sz[4];
-          mma_16816_c(sz, za0, 0u, za2, 0u, zw, zw, 0.f, 0.f, 0.f, 0.f);
+          mma_16816_c(sz, za0, za0, za2, za2, zw, zw, 0.f, 0.f, 0.f, 0.f);
           float2 tot = make_float2(sz[0], sz[1]);
-          // two groups per accumulator: the even one's rows are 0..7, the odd
-          // one's 8..15
 #pragma unroll
           for (int c = 0; c < NG; c += 2) {
-            float a[4];
+            // group c in the accumulator's rows 0..7, group c + 1 in the other's 8..15
+            float x[4], y[4];
             const uint32_t w0 = kc[nb][c], w1 = kc[nb][c + 1];
-            mma_16816_c(a, qa[c][0], 0u, qa[c][1], 0u, kc4.pair(w0, 0), kc4.pair(w0, 1), qinit[c][0], qinit[c][1],
-                        qinit[c + 1][0], qinit[c + 1][1]);
-            mma_16816(a, qa[c][2], 0u, qa[c][3], 0u, kc4.pair(w0, 2), kc4.pair(w0, 3));
-            mma_16816(a, 0u, qa[c + 1][0], 0u, qa[c + 1][1], kc4.pair(w1, 0), kc4.pair(w1, 1));
-            mma_16816(a, 0u, qa[c + 1][2], 0u, qa[c + 1][3], kc4.pair(w1, 2), kc4.pair(w1, 3));
-            tot = __ffma2_rn(make_float2(bf16_lo(s0[c / 2]), bf16_lo(s1[c / 2])), make_float2(a[0], a[1]), tot);
-            tot = __ffma2_rn(make_float2(bf16_hi(s0[c / 2]), bf16_hi(s1[c / 2])), make_float2(a[2], a[3]), tot);
+            mma_16816_c(x, qa[c][0], qa[c + 1][0], qa[c][1], qa[c + 1][1], kc4.pair(w0, 0), kc4.pair(w0, 1),
+                        qinit[c][0], qinit[c][1], qinit[c + 1][0], qinit[c + 1][1]);
+            mma_16816_c(y, qa[c][0], qa[c + 1][0], qa[c][1], qa[c + 1][1], kc4.pair(w1, 0), kc4.pair(w1, 1),
+                        qinit[c][0], qinit[c][1], qinit[c + 1][0], qinit[c + 1][1]);
+            mma_16816(x, qa[c][2], qa[c + 1][2], qa[c][3], qa[c + 1][3], kc4.pair(w0, 2), kc4.pair(w0, 3));
+            mma_16816(y, qa[c][2], qa[c + 1][2], qa[c][3], qa[c + 1][3], kc4.pair(w1, 2), kc4.pair(w1, 3));
+            tot = __ffma2_rn(make_float2(bf16_lo(s0[c / 2]), bf16_lo(s1[c / 2])), make_float2(x[0], x[1]), tot);
+            tot = __ffma2_rn(make_float2(bf16_hi(s0[c / 2]), bf16_hi(s1[c / 2])), make_float2(y[2], y[3]), tot);
           }
-          sc[2 * nb] = tot.x * p.scale_log2;
-          sc[2 * nb + 1] = tot.y * p.scale_log2;
+          sc[u][nb] = __fmul2_rn(tot, make_float2(p.scale_log2, p.scale_log2));
         }
-        if (!whole) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!visible(key0 + kw + 8 * (e >> 1) + 2 * t4 + (e & 1))) sc[e] = -INFINITY;
-        }
-
-        // ---- online softmax with a lazily moved reference, as elsewhere
-        float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const bool move = mx > m_run + C::RESCALE_THRESHOLD || (m_run == -INFINITY && mx != -INFINITY);
-        if (__any_sync(0xffffffffu, move)) {
-          float alpha = 1.f;
-          if (move) {
-            alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - mx);
-            m_run = mx;
-            l_part *= alpha;
-          }
-          const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t4);      // row 2t
-          const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);  // row 2t + 1
-#pragma unroll
-          for (int c = 0; c < NG; ++c)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) oacc[c][k][e] *= (e & 1) ? a1 : a0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) zacc[e] *= (e & 1) ? a1 : a0;
-        }
-        const float ref = m_run == -INFINITY ? 0.f : m_run;
-        float pv[4];
+      }
+      if (!whole) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          pv[e] = ex2_approx(sc[e] - ref);
-          l_part += pv[e];
+          const int key = ks + 8 * e + 2 * t4;
+          if (!visible(key)) sc[e >> 1][e & 1].x = -INFINITY;
+          if (!visible(key + 1)) sc[e >> 1][e & 1].y = -INFINITY;
         }
+      }
 
-        // ---- O^T += V^T P^T
-        const uint32_t vp = st + C::OFF_VP + kw * C::PB;
+      // ---- online softmax with a lazily moved reference, as elsewhere
+      float mx = fmaxf(fmax3(sc[0][0].x, sc[0][0].y, sc[0][1].x), fmax3(sc[0][1].y, sc[1][0].x, sc[1][0].y));
+      mx = fmax3(mx, sc[1][1].x, sc[1][1].y);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const bool move = mx > m_run + C::RESCALE_THRESHOLD || (m_run == -INFINITY && mx != -INFINITY);
+      if (__any_sync(0xffffffffu, move)) {
+        float alpha = 1.f;
+        if (move) {
+          alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - mx);
+          m_run = mx;
+          l_part *= alpha;
+        }
+        const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t4);      // row 2t
+        const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);  // row 2t + 1
+#pragma unroll
+        for (int c = 0; c < NG; ++c)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) oacc[c][k][e] *= (e & 1) ? a1 : a0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zacc[e] *= (e & 1) ? a1 : a0;
+      }
+      const float ref = m_run == -INFINITY ? 0.f : m_run;
+      float2 pv[2][2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = sc[e >> 1][e & 1];
+        pv[e >> 1][e & 1] = make_float2(ex2_approx(x.x - ref), ex2_approx(x.y - ref));
+      }
+      const float2 lsum = __fadd2_rn(__fadd2_rn(pv[0][0], pv[0][1]), __fadd2_rn(pv[1][0], pv[1][1]));
+      l_part += lsum.x + lsum.y;
+
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t vp = st + C::OFF_VP + 16 * u * C::PB;
         uint32_t sv[4][NG / 2];
 #pragma unroll
         for (int e = 0; e < 4; ++e) kv4_steps<NG>(vp + (8 * (e >> 1) + 2 * t4 + (e & 1)) * C::PB, sv[e]);
         {
-          uint32_t z0, z1;
+          uint32_t z0, z1, z2, z3;
           if constexpr (NG == 4) {
-            // row g: the steps (0..3, not wanted) and the centres (4..7)
-            ldsm_x2_t(vp + (lane & 15) * C::PB, z0, z1);
+            // row g: the steps (0..3, not wanted) and the centres (4..7) of keys
+            // 2t, 2t + 1; rows 8..15 the same again
+            ldsm_x4_t(vp + (((lane >> 4) << 3) + (lane & 7)) * C::PB, z0, z1, z2, z3);
           } else {
             const uint32_t a = vp + 2 * t4 * C::PB + 4;  // the centres' words of keys 2t, 2t + 1 (+ 8)
             const uint32_t sel = g == 0 ? 0x5410u : 0x7632u;
             z0 = __byte_perm(lds32(a), lds32(a + C::PB), sel);
-            z1 = __byte_perm(lds32(a + 8 * C::PB), lds32(a + 9 * C::PB), sel);
-            if (g > 1) z0 = z1 = 0u;
+            z2 = __byte_perm(lds32(a + 8 * C::PB), lds32(a + 9 * C::PB), sel);
+            z1 = z0;
+            z3 = z2;
           }
-          mma_16816(zacc, z0, 0u, z1, 0u, pack_bf16x2(pv[0], pv[1]), pack_bf16x2(pv[2], pv[3]));
+          mma_16816(zacc, z0, z1, z2, z3, pack_bf16x2(pv[u][0].x, pv[u][0].y), pack_bf16x2(pv[u][1].x, pv[u][1].y));
         }
 #pragma unroll
         for (int c2 = 0; c2 < NG; c2 += 2) {
           uint32_t vc[2][2];  // [group of the two][keys 0..7, 8..15]
-          ldsm_x4_t(st + C::OFF_V + kv4_swz<D>(kw + ((lane >> 3) & 1) * 8 + (lane & 7), c2 + (lane >> 4)), vc[0][0],
-                    vc[0][1], vc[1][0], vc[1][1]);
+          ldsm_x4_t(st + C::OFF_V + kv4_swz<D>(16 * u + ((lane >> 3) & 1) * 8 + (lane & 7), c2 + (lane >> 4)),
+                    vc[0][0], vc[0][1], vc[1][0], vc[1][1]);
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
             const int c = c2 + cc;
-            float ps[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) ps[e] = pv[e] * (cc ? bf16_hi(sv[e][c2 / 2]) : bf16_lo(sv[e][c2 / 2]));
-            const uint32_t b0 = pack_bf16x2(ps[0], ps[1]), b1 = pack_bf16x2(ps[2], ps[3]);
+            const float2 f0 = cc ? make_float2(bf16_hi(sv[0][c2 / 2]), bf16_hi(sv[1][c2 / 2]))
+                                 : make_float2(bf16_lo(sv[0][c2 / 2]), bf16_lo(sv[1][c2 / 2]));
+            const float2 f1 = cc ? make_float2(bf16_hi(sv[2][c2 / 2]), bf16_hi(sv[3][c2 / 2]))
+                                 : make_float2(bf16_lo(sv[2][c2 / 2]), bf16_lo(sv[3][c2 / 2]));
+            const float2 p0 = __fmul2_rn(pv[u][0], f0), p1 = __fmul2_rn(pv[u][1], f1);
+            const uint32_t b0 = pack_bf16x2(p0.x, p0.y), b1 = pack_bf16x2(p1.x, p1.y);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
               mma_16816(oacc[c][k], kc4.pair_c(vc[cc][0], 2 * k), kc4.pair_c(vc[cc][0], 2 * k + 1),
