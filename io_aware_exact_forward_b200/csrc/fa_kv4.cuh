@@ -402,6 +402,15 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
   bool ok = true;
   uint32_t phases = 0;  // bit s: parity of the next use of stage s
 
+  // Lane offsets into a stage; rows 8 or 16 further on have the same swizzle,
+  // and the second pair of V's chunks is the first with chunk bit 1 flipped.
+  const uint32_t off_k = C::OFF_K + (D == 128 ? kv4_swz<D>(lane & 7, lane >> 3)
+                                              : kv4_swz<D>(((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1));
+  const uint32_t off_v = C::OFF_V + kv4_swz<D>(((lane >> 3) & 1) * 8 + (lane & 7), lane >> 4);
+  const uint32_t off_kz = C::OFF_KP + g * C::PB + 2 * NG + (NG == 4 ? 4 * (t4 & 1) : 0);
+  const uint32_t off_ks = C::OFF_KP + 2 * t4 * C::PB;
+  const uint32_t off_vz = C::OFF_VP + (((lane >> 4) << 3) + (lane & 7)) * C::PB;
+
   auto key_of = [&](const Kv4Stretch& sg, int j) { return (j < sg.n_sink ? sg.key_a : sg.key_b) + j * C::TILE; };
   auto needed = [&](const Kv4Stretch& sg, int ks) {
     return ks < sg.len && (ks + C::SLICE > sg.lo || ks < p.sinks);
@@ -523,19 +532,16 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
         if constexpr (D == 128) {
 #pragma unroll
           for (int nb = 0; nb < 2; ++nb)
-            ldsm_x4(st + C::OFF_K + kv4_swz<D>(16 * u + 8 * nb + (lane & 7), lane >> 3), kc[nb][0], kc[nb][1],
-                    kc[nb][2], kc[nb][3]);
+            ldsm_x4(st + off_k + (16 * u + 8 * nb) * C::CB, kc[nb][0], kc[nb][1], kc[nb][2], kc[nb][3]);
         } else {
-          ldsm_x4(st + C::OFF_K + kv4_swz<D>(16 * u + ((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1), kc[0][0],
-                  kc[0][1], kc[1][0], kc[1][1]);
+          ldsm_x4(st + off_k + 16 * u * C::CB, kc[0][0], kc[0][1], kc[1][0], kc[1][1]);
         }
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb) {
-          const uint32_t kp = st + C::OFF_KP + (16 * u + 8 * nb) * C::PB;
-          const uint32_t zw = lds32(kp + g * C::PB + 2 * NG + (NG == 4 ? 4 * (t4 & 1) : 0));
+          const uint32_t zw = lds32(st + off_kz + (16 * u + 8 * nb) * C::PB);
           uint32_t s0[NG / 2], s1[NG / 2];
-          kv4_steps<NG>(kp + (2 * t4) * C::PB, s0);
-          kv4_steps<NG>(kp + (2 * t4 + 1) * C::PB, s1);
+          kv4_steps<NG>(st + off_ks + (16 * u + 8 * nb) * C::PB, s0);
+          kv4_steps<NG>(st + off_ks + (16 * u + 8 * nb + 1) * C::PB, s1);
           float sz[4];
           mma_16816_c(sz, za0, za0, za2, za2, zw, zw, 0.f, 0.f, 0.f, 0.f);
           float2 tot = make_float2(sz[0], sz[1]);
@@ -602,18 +608,18 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
       // ---- O^T += V^T P^T
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint32_t vp = st + C::OFF_VP + 16 * u * C::PB;
+        const uint32_t vs = st + off_ks + (C::OFF_VP - C::OFF_KP) + 16 * u * C::PB;
         uint32_t sv[4][NG / 2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) kv4_steps<NG>(vp + (8 * (e >> 1) + 2 * t4 + (e & 1)) * C::PB, sv[e]);
+        for (int e = 0; e < 4; ++e) kv4_steps<NG>(vs + (8 * (e >> 1) + (e & 1)) * C::PB, sv[e]);
         {
           uint32_t z0, z1, z2, z3;
           if constexpr (NG == 4) {
             // row g: the steps (0..3, not wanted) and the centres (4..7) of keys
             // 2t, 2t + 1; rows 8..15 the same again
-            ldsm_x4_t(vp + (((lane >> 4) << 3) + (lane & 7)) * C::PB, z0, z1, z2, z3);
+            ldsm_x4_t(st + off_vz + 16 * u * C::PB, z0, z1, z2, z3);
           } else {
-            const uint32_t a = vp + 2 * t4 * C::PB + 4;  // the centres' words of keys 2t, 2t + 1 (+ 8)
+            const uint32_t a = vs + 4;  // the centres' words of keys 2t, 2t + 1 (+ 8)
             const uint32_t sel = g == 0 ? 0x5410u : 0x7632u;
             z0 = __byte_perm(lds32(a), lds32(a + C::PB), sel);
             z2 = __byte_perm(lds32(a + 8 * C::PB), lds32(a + 9 * C::PB), sel);
@@ -625,8 +631,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
 #pragma unroll
         for (int c2 = 0; c2 < NG; c2 += 2) {
           uint32_t vc[2][2];  // [group of the two][keys 0..7, 8..15]
-          ldsm_x4_t(st + C::OFF_V + kv4_swz<D>(16 * u + ((lane >> 3) & 1) * 8 + (lane & 7), c2 + (lane >> 4)),
-                    vc[0][0], vc[0][1], vc[1][0], vc[1][1]);
+          ldsm_x4_t(((st + off_v) ^ (16 * c2)) + 16 * u * C::CB, vc[0][0], vc[0][1], vc[1][0], vc[1][1]);
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
             const int c = c2 + cc;
