@@ -283,6 +283,13 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
   return r;
 }
+// D = A B with k = 8.
+__device__ __forceinline__ void mma_1688_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+}
 // D = A B + C with C apart from D, so that a constant C stays in its registers.
 __device__ __forceinline__ void mma_16816_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
@@ -447,7 +454,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
     // four registers that stay)
     uint32_t qa[NG][4];
     float qinit[NG][2];   // -136 sum of the group's q, twice: the accumulator's two columns
-    uint32_t za0, za2 = 0u;
+    uint32_t za0, za1 = 0u;  // sum q: parts 0 and 1 in row g, part 2 in row g + 8
     {
       const __nv_bfloat16* qrow = p.q + ((size_t)sg.pair * G + (g < G ? g : 0)) * D;
       float qs[NG];
@@ -482,7 +489,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
       }
       if constexpr (NG == 4) {
         za0 = t4 == 0 ? part[0][0] : t4 == 1 ? part[0][1] : t4 == 2 ? part[1][0] : part[1][1];
-        za2 = t4 == 0 ? part[2][0] : t4 == 1 ? part[2][1] : 0u;
+        za1 = t4 == 0 ? part[2][0] : t4 == 1 ? part[2][1] : 0u;
       } else {
         za0 = t4 == 0 ? part[0][0] : t4 == 1 ? part[1][0] : t4 == 2 ? part[2][0] : 0u;
       }
@@ -543,8 +550,9 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
           kv4_steps<NG>(st + off_ks + (16 * u + 8 * nb) * C::PB, s0);
           kv4_steps<NG>(st + off_ks + (16 * u + 8 * nb + 1) * C::PB, s1);
           float sz[4];
-          mma_16816_c(sz, za0, za0, za2, za2, zw, zw, 0.f, 0.f, 0.f, 0.f);
-          float2 tot = make_float2(sz[0], sz[1]);
+          mma_1688_z(sz, za0, za1, zw);
+          float2 tot = NG == 4 ? __fadd2_rn(make_float2(sz[0], sz[1]), make_float2(sz[2], sz[3]))
+                               : make_float2(sz[0], sz[1]);
 #pragma unroll
           for (int c = 0; c < NG; c += 2) {
             // group c in the accumulator's rows 0..7, group c + 1 in the other's 8..15
