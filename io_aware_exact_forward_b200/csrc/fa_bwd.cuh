@@ -30,6 +30,8 @@
 //                dQ_tile lands in the dP^T columns, so the next dP^T follows
 //                the dQ read-out.  A sliding window is a separate
 //                instantiation (its masking costs registers).
+//                With sinks P^T is kept twice in the S^T columns, in bf16 for
+//                dV's product and in fp16 for the dS warps.
 //                dQ_tile is read by a second warpgroup, staged in shared
 //                memory and added into an fp32 accumulator in global memory
 //                with bulk tensor reduce-adds (every KV tile contributes to
@@ -44,6 +46,8 @@
 // The deterministic backward builds dkdv without dQ (DQ = false: no dQ
 // product, warps 16-19 idle) and takes dQ from the pass in fa_bwd_dq.cuh.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "fa_ptx.cuh"
 
@@ -126,6 +130,11 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_convert_kernel(const float* __r
 // ---------------------------------------------------------------------------
 // dK / dV (+ dQ contributions)
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 struct BwdParams {
   CUtensorMap tm_q;    // [B][Tq][Hq][d] bf16, box {64,1,128,1}, 128-byte swizzle
   CUtensorMap tm_do;
@@ -343,6 +352,9 @@ __device__ __forceinline__ void dropout_keep_keyrow_64(uint32_t (&mask)[2], int 
 template <int D, int WIN, bool DROP = false, bool DQ = true>
 __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
   using C = BwdCfg<D, DROP, DQ>;
+  // two copies of P^T in the S^T columns: the dropped and the undropped one, or,
+  // with sinks, bf16 for dV's product and fp16 for dS
+  constexpr bool TWO_P = DROP || WIN == 2;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {  // the layout needs 1024-byte aligned swizzle atoms
@@ -603,10 +615,10 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
             issue_s(gi + 1, kvb_next);
           }
           // P^T of query half h sits in columns [64h, 64h+32) of the S^T
-          // buffer; with dropout the dropped P^T of chunk c (16 queries) in
-          // columns 64h + 16c .. + 7.
+          // buffer; with dropout (sinks) the dropped (bf16) P^T of chunk c (16
+          // queries) in columns 64h + 16c .. + 7.
           auto p_col = [](int k) {
-            return DROP ? ((k < 4) ? k * 16 : 64 + (k - 4) * 16) : ((k < 4) ? k * 8 : 64 + (k - 4) * 8);
+            return TWO_P ? ((k < 4) ? k * 16 : 64 + (k - 4) * 16) : ((k < 4) ? k * 8 : 64 + (k - 4) * 8);
           };
           ok = mbar_wait(bar_p_full(buf), (gi / C::NSBUF) & 1, wc);
           if (!ok) break;
@@ -742,6 +754,7 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
           if (c + 1 < 4) tmem_ld16(tS + (c + 1) * 16, sv[(c + 1) & 1]);
           const uint32_t* cur = sv[c & 1];
           uint32_t pk[8];
+          uint32_t ph[WIN == 2 ? 8 : 1];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int col = c * 16 + 2 * e;
@@ -755,8 +768,14 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
               if (!key_ok || col + 1 < cmin || (WIN && col + 1 >= cmax)) p1 = 0.f;
             }
             pk[e] = pack_bf16x2(p0, p1);
+            if constexpr (WIN == 2) ph[e] = pack_f16x2(p0, p1);
           }
-          if constexpr (DROP) {
+          if constexpr (WIN == 2) {
+            // P is at most 1, so fp16 holds it to 2^-12 of itself (2^-25 below
+            // 2^-14): dS = P (dP - D) is then rounded to bf16 once, not twice
+            tmem_st8(tS + c * 16 + 8, ph);
+            tmem_st8(tS + c * 16, pk);
+          } else if constexpr (DROP) {
             // undropped P^T beside the dropped one, both over this chunk's
             // own (already loaded) S^T columns
             tmem_st8(tS + c * 16 + 8, pk);
@@ -875,6 +894,9 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
               keep[c >> 1] |= (((pd[e] & 0xFFFFu) != 0u ? 1u : 0u) | ((pd[e] >> 16) != 0u ? 2u : 0u))
                               << (16 * (c & 1) + 2 * e);
           }
+        } else if constexpr (WIN == 2) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld8(tP + 16 * c + 8, pp + 8 * c);
         } else {
           tmem_ld32(tP, pp);
         }
@@ -899,7 +921,11 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 pf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&pp[8 * c + e]));
+            float2 pf;
+            if constexpr (WIN == 2)
+              pf = __half22float2(*reinterpret_cast<const __half2*>(&pp[8 * c + e]));
+            else
+              pf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&pp[8 * c + e]));
             const float2 dd = *reinterpret_cast<const float2*>(drow + 16 * c + 2 * e);
             float2 t;
             if constexpr (DROP) {
