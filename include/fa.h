@@ -324,9 +324,12 @@ int fa_decode_splitkv_window(const void* q, const void* k_cache, const void* v_c
  * fa_forward_sinks: the query sees the last `window` cached keys and the first
  * `sinks` of its sequence.  sinks = 0 gives fa_decode_splitkv_window; outside
  * [0, 1024] it is FA_ERR_INVALID_ARG.  With sinks > 0, cache rows that the query
- * does not see may hold anything, NaN included.  Other arguments, workspace and
+ * does not see may hold anything, NaN included.  The workspace needs
+ * fa_decode_sinks_workspace_bytes(): the partials of the chunks that can be
+ * visible, never more than fa_decode_workspace_bytes().  Other arguments and
  * errors as fa_decode_splitkv_window.
  */
+size_t fa_decode_sinks_workspace_bytes(int B, int Hq, int Tk_max, int d, int chunk, int window, int sinks);
 int fa_decode_splitkv_sinks(const void* q, const void* k_cache, const void* v_cache,
                             const int* seqlens_k, void* o, float* lse, void* ws, size_t ws_bytes,
                             int B, int Hq, int Hkv, int Tk_max, int d, float scale, int chunk,

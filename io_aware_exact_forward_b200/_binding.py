@@ -61,6 +61,7 @@ SIGNATURES = {
     "fa_forward_sinks": (_c_int, [_vp] * 5 + [_c_int] * 6 + [_c_float, _c_int, _c_int, _vp]),
     "fa_backward_sinks_workspace_bytes": (_c_size, [_c_int] * 8),
     "fa_backward_sinks": (_c_int, [_vp] * 9 + [_vp, _c_size] + [_c_int] * 6 + [_c_float] + [_c_int] * 3 + [_vp]),
+    "fa_decode_sinks_workspace_bytes": (_c_size, [_c_int] * 7),
     "fa_decode_splitkv_sinks": (_c_int, [_vp] * 6 + [_vp, _c_size] + [_c_int] * 5 + [_c_float] + [_c_int] * 3 + [_vp]),
     "fa_rope": (_c_int, [_vp] * 7 + [_c_int] * 2 + [_c_float] + [_c_int] * 5 + [_vp]),
     "fa_rope_backward": (_c_int, [_vp] * 7 + [_c_int] * 2 + [_c_float] + [_c_int] * 5 + [_vp]),
@@ -131,12 +132,33 @@ def _need_window(window, sinks):
         raise ValueError("sinks need a window (without one every key is visible)")
 
 
-def _on_device(device):
-    """Guard that makes ``device`` the current one where it is not: a launch on
-    another device's stream fails, and kernel attributes are per device."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _on_device(index):
+    """Guard that makes device ``index`` the current one where it is not: a launch
+    on another device's stream fails, and kernel attributes are per device."""
+    return _NO_GUARD if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+
+
+def _stream_of(index):
+    """The current stream of device ``index``, as torch.cuda.current_stream gives
+    it, without making a Stream object of it (a decode step is a few such calls
+    long)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _fits(t, dtype, index, shape):
+    """Whether t is a dense tensor of this type, device and shape: _check_dev and
+    _check_out in one, for the calls that are made once per token."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape
+            and t.is_contiguous())
+
+
+def _demand(name, t, dtype, index, shape):
+    if not _fits(t, dtype, index, shape):
+        _check_dev(name, t, dtype, torch.device("cuda", index))
+        _check_out(name, t, shape)
 
 
 def forward(q, k, v, scale=None, causal=False, out=None, lse=None, window=None, sinks=0):
@@ -165,7 +187,7 @@ def forward(q, k, v, scale=None, causal=False, out=None, lse=None, window=None, 
         _raise("fa_forward", st)
     elif sinks:
         _check_kv_shapes(q, k, v)
-        with _on_device(dev):
+        with _on_device(dev.index):
             st = lib.fa_forward_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Tq, Tk, d,
                                       float(scale), int(window), int(sinks), _stream_ptr(dev))
         _raise("fa_forward_sinks", st)
@@ -276,7 +298,7 @@ def backward(q, k, v, o, lse, do, scale=None, causal=False, workspace=None, dq=N
             _check_dev(n, t, torch.bfloat16, dev)
             _check_out(n, t, like.shape)
         _check_out("lse", lse, (B, Hq, Tq))
-        with _on_device(dev):
+        with _on_device(dev.index):
             st = lib.fa_backward_sinks(*args, int(window), int(sinks), int(bool(deterministic)), _stream_ptr(dev))
         _raise("fa_backward_sinks", st)
     elif deterministic:
@@ -329,8 +351,10 @@ def decode_splitkv(q, k_cache, v_cache, seqlens, scale=None, chunk=256, workspac
     """Split-KV decode.  q [B,Hq,d], caches [B,Tk_max,Hkv,d] bf16, seqlens int32 [B] (CUDA).
     ``window`` (int >= 1) keeps only the last `window` keys of each sequence, and
     ``sinks`` its first ones with them (fa_decode_splitkv_sinks)."""
+    if sinks:
+        _need_window(window, sinks)
+        return _decode_sinks(q, k_cache, v_cache, seqlens, scale, chunk, workspace, out, lse, window, sinks)
     lib = load_library()
-    _need_window(window, sinks)
     B, Hq, d = q.shape
     Tk_max, Hkv = k_cache.shape[1], k_cache.shape[2]
     dev = q.device
@@ -349,24 +373,52 @@ def decode_splitkv(q, k_cache, v_cache, seqlens, scale=None, chunk=256, workspac
     if window is None:
         st = lib.fa_decode_splitkv(*args, _stream_ptr(dev))
         _raise("fa_decode_splitkv", st)
-    elif sinks:
-        _check_kv_shapes(q, k_cache, v_cache)
-        _check_decode_out(q, seqlens, out, lse)
-        with _on_device(dev):
-            st = lib.fa_decode_splitkv_sinks(*args, int(window), int(sinks), _stream_ptr(dev))
-        _raise("fa_decode_splitkv_sinks", st)
     else:
         st = lib.fa_decode_splitkv_window(*args, int(window), _stream_ptr(dev))
         _raise("fa_decode_splitkv_window", st)
     return out, lse
 
 
-def _check_decode_out(q, seqlens, out, lse):
-    _check_dev("out", out, torch.bfloat16, q.device)
-    _check_dev("lse", lse, torch.float32, q.device)
-    _check_out("out", out, q.shape)
-    _check_out("lse", lse, q.shape[:2])
-    _check_out("seqlens", seqlens, q.shape[:1])
+def _cuda_index(name, t):
+    """Device index of a CUDA tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be on a CUDA device (libfa has no CPU path)")
+    return index
+
+
+def _decode_sinks(q, k_cache, v_cache, seqlens, scale, chunk, workspace, out, lse, window, sinks):
+    lib = load_library()
+    index = _cuda_index("q", q)
+    B, Hq, d = q.shape
+    Tk_max, Hkv = k_cache.shape[1], k_cache.shape[2]
+    _demand("q", q, torch.bfloat16, index, (B, Hq, d))
+    _demand("k_cache", k_cache, torch.bfloat16, index, (B, Tk_max, Hkv, d))
+    _demand("v_cache", v_cache, torch.bfloat16, index, (B, Tk_max, Hkv, d))
+    _demand("seqlens", seqlens, torch.int32, index, (B,))
+    if workspace is None:
+        need = lib.fa_decode_sinks_workspace_bytes(B, Hq, Tk_max, d, chunk, window, sinks)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    else:
+        _check_dev("workspace", workspace, torch.uint8, q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _demand("out", out, torch.bfloat16, index, (B, Hq, d))
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _demand("lse", lse, torch.float32, index, (B, Hq))
+    with _on_device(index):
+        st = lib.fa_decode_splitkv_sinks(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), seqlens.data_ptr(),
+                                         out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(), B, Hq,
+                                         Hkv, Tk_max, d, d ** -0.5 if scale is None else scale, chunk, window, sinks,
+                                         _stream_of(index))
+    if st:
+        _raise("fa_decode_splitkv_sinks", st)
+    return out, lse
 
 
 def decode_splitkv_noalloc(q, k_cache, v_cache, seqlens, scale=None, chunk=256, out=None, lse=None):

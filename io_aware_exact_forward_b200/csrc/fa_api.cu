@@ -714,10 +714,28 @@ int fa_backward_sinks(const void* q, const void* k, const void* v, const void* o
 
 static size_t decode_nchunk(int Tk_max, int chunk) { return ((size_t)Tk_max + chunk - 1) / chunk; }
 
+static size_t decode_ws_bytes(int B, int Hq, size_t n, int d) {
+  return round256((size_t)B * Hq * n * d * 4) + round256((size_t)B * Hq * n * 4);
+}
+
 size_t fa_decode_workspace_bytes(int B, int Hq, int Tk_max, int d, int chunk) {
   if (B < 0 || Hq < 1 || Tk_max < 0 || chunk < 1 || (d != 64 && d != 128)) return 0;
-  const size_t n = decode_nchunk(Tk_max, chunk);
-  return round256((size_t)B * Hq * n * d * 4) + round256((size_t)B * Hq * n * 4);
+  return decode_ws_bytes(B, Hq, decode_nchunk(Tk_max, chunk), d);
+}
+
+// Chunks of a sequence that can be visible: those that hold sinks and those
+// that a window can touch.
+static size_t decode_visible_chunks(int Tk_max, int chunk, int window, int sinks) {
+  return std::min(decode_nchunk(Tk_max, chunk),
+                  (size_t)(sinks + chunk - 1) / chunk + ((size_t)window + chunk - 2) / chunk + 1);
+}
+
+size_t fa_decode_sinks_workspace_bytes(int B, int Hq, int Tk_max, int d, int chunk, int window, int sinks) {
+  if (B < 0 || Hq < 1 || Tk_max < 0 || chunk < 1 || (d != 64 && d != 128) || window < 1 || sinks < 0 ||
+      sinks > kMaxSinks)
+    return 0;
+  return decode_ws_bytes(B, Hq, sinks > 0 ? decode_visible_chunks(Tk_max, chunk, window, sinks)
+                                          : decode_nchunk(Tk_max, chunk), d);
 }
 
 }  // extern "C"
@@ -743,17 +761,14 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache, 
   if (!aligned16(q) || !aligned16(o ? o : o32) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(seqlens_k) & 3u) ||
       (Tk_max > 0 && (!aligned16(k_cache) || !aligned16(v_cache))))
     return FA_ERR_ALIGNMENT;
-  const size_t need = fa_decode_workspace_bytes(B, Hq, Tk_max, d, chunk);
+  // with sinks, only the chunks that can be visible are items
+  const size_t n = sinks > 0 ? decode_visible_chunks(Tk_max, chunk, window, sinks) : decode_nchunk(Tk_max, chunk);
+  const size_t need = decode_ws_bytes(B, Hq, n, d);
   if (!ws || ws_bytes < need || !aligned16(ws)) return FA_ERR_WORKSPACE;
   int st = device_setup();
   if (st) return st;
   DecodeParams p;
   memset(&p, 0, sizeof(p));
-  size_t n = decode_nchunk(Tk_max, chunk);
-  // with sinks, only the visible chunks are items: those that hold sinks and
-  // those that a window can touch
-  if (sinks > 0)
-    n = std::min(n, (size_t)(sinks + chunk - 1) / chunk + ((size_t)window + chunk - 2) / chunk + 1);
   if (Tk_max > 0) {
     st = make_tmap_4d(&p.tm_k, k_cache, d, Hkv, Tk_max, B, 64, 64, true);
     if (!st) st = make_tmap_4d(&p.tm_v, v_cache, d, Hkv, Tk_max, B, 64, 64, true);

@@ -16,8 +16,7 @@ from typing import NamedTuple
 
 import torch
 
-from ._binding import (_check_decode_out, _check_dev, _check_out, _on_device, _ptr, _raise, _stream_ptr,
-                       load_library)
+from ._binding import _check_dev, _cuda_index, _demand, _on_device, _raise, _stream_of, load_library
 
 __all__ = ["KV4Cache", "kv4_cache", "kv4_append", "kv4_read", "kv4_decode", "kv4_decode_workspace_bytes"]
 
@@ -51,22 +50,31 @@ def kv4_cache(B, Hkv, Tk_max, d, device="cuda"):
     return KV4Cache(codes(), params(), codes(), params())
 
 
-def _cache_sizes(cache, dev):
+def _cache_sizes(cache, index):
     kc, kp, vc, vp = cache
     if kc.dim() != 4:
         raise ValueError(f"k_codes must be [B, Hkv, Tk_max, d/2], got {tuple(kc.shape)}")
-    B, Hkv, Tk, d = kc.shape[0], kc.shape[1], kc.shape[2], 2 * kc.shape[3]
-    for n, t, dt, w in (("k_codes", kc, torch.uint8, d // 2), ("k_params", kp, torch.bfloat16, 2 * (d // GROUP)),
-                        ("v_codes", vc, torch.uint8, d // 2), ("v_params", vp, torch.bfloat16, 2 * (d // GROUP))):
-        _check_dev(n, t, dt, dev)
-        _check_out(n, t, (B, Hkv, Tk, w))
-    return B, Hkv, Tk, d
+    B, Hkv, Tk, w = codes = kc.shape
+    params = (B, Hkv, Tk, 4 * w // GROUP)
+    _demand("k_codes", kc, torch.uint8, index, codes)
+    _demand("k_params", kp, torch.bfloat16, index, params)
+    _demand("v_codes", vc, torch.uint8, index, codes)
+    _demand("v_params", vp, torch.bfloat16, index, params)
+    return B, Hkv, Tk, 2 * w
 
 
-def _check_counts(name, t, B, dev):
-    if t is not None:
-        _check_dev(name, t, torch.int32, dev)
-        _check_out(name, t, (B,))
+def _counts(start, count, B, index):
+    """Pointers of start and count (0 for none)."""
+    if start is None:
+        raise TypeError("start must be an int32 tensor")
+    _demand("start", start, torch.int32, index, (B,))
+    if count is None:
+        return start.data_ptr(), 0
+    _demand("count", count, torch.int32, index, (B,))
+    return start.data_ptr(), count.data_ptr()
+
+
+_STRIDES = ctypes.c_longlong * 6
 
 
 def kv4_append(k, v, cache, start, count=None):
@@ -75,47 +83,53 @@ def kv4_append(k, v, cache, start, count=None):
     ``start`` int32 [B] (CUDA); ``count`` int32 [B]: only rows t < count[b] are
     written.  Rows outside the cache are dropped."""
     lib = load_library()
-    dev = k.device
-    B, Hkv, Tk, d = _cache_sizes(cache, dev)
+    index = _cuda_index("k", k)
+    B, Hkv, Tk, d = _cache_sizes(cache, index)
+    T = k.shape[1] if k.dim() == 4 else 0
+    strides = []
     for n, t in (("k", k), ("v", v)):
-        if t.device.type != "cuda" or t.device != dev:
-            raise ValueError(f"{n} must be on {dev}, a CUDA device")
-        if t.dtype != torch.bfloat16:
+        if _cuda_index(n, t) != index:
+            raise ValueError(f"{n} is on {t.device}, expected cuda:{index}")
+        if t.dtype is not torch.bfloat16:
             raise TypeError(f"{n} must be {torch.bfloat16}, got {t.dtype}")
-        if t.dim() != 4 or t.shape != (B, k.shape[1], Hkv, d):
+        if t.shape != (B, T, Hkv, d):
             raise ValueError(f"{n} must be [{B}, T, {Hkv}, {d}], got {tuple(t.shape)}")
-        if t.stride(3) != 1:
+        st = t.stride()
+        if st[3] != 1:
             raise ValueError(f"{n} must be contiguous in its last dim")
-    if start is None:
-        raise TypeError("start must be an int32 tensor")
-    _check_counts("start", start, B, dev)
-    _check_counts("count", count, B, dev)
-    strides = (ctypes.c_longlong * 6)(*(0 if t.shape[i] == 1 else t.stride(i) for t in (k, v) for i in range(3)))
-    with _on_device(dev):
-        st = lib.fa_kv4_append(k.data_ptr(), v.data_ptr(), strides, *(t.data_ptr() for t in cache), start.data_ptr(),
-                               _ptr(count), B, k.shape[1], Hkv, Tk, d, _stream_ptr(dev))
-    _raise("fa_kv4_append", st)
+        # no address depends on the stride of a dim of size 1
+        strides += (0 if B == 1 else st[0], 0 if T == 1 else st[1], 0 if Hkv == 1 else st[2])
+    start_ptr, count_ptr = _counts(start, count, B, index)
+    kc, kp, vc, vp = cache
+    with _on_device(index):
+        st = lib.fa_kv4_append(k.data_ptr(), v.data_ptr(), _STRIDES(*strides), kc.data_ptr(), kp.data_ptr(),
+                               vc.data_ptr(), vp.data_ptr(), start_ptr, count_ptr, B, T, Hkv, Tk, d, _stream_of(index))
+    if st:
+        _raise("fa_kv4_append", st)
 
 
 def kv4_read(cache, start, T, count=None, out_k=None, out_v=None):
     """k, v bf16 [B,T,Hkv,d]: the cache's values at positions start[b] + t.
     Rows t >= count[b], or outside the cache, read as zeros."""
     lib = load_library()
-    dev = cache[0].device
-    B, Hkv, Tk, d = _cache_sizes(cache, dev)
-    if start is None:
-        raise TypeError("start must be an int32 tensor")
-    _check_counts("start", start, B, dev)
-    _check_counts("count", count, B, dev)
-    out_k = torch.empty((B, T, Hkv, d), dtype=torch.bfloat16, device=dev) if out_k is None else out_k
-    out_v = torch.empty((B, T, Hkv, d), dtype=torch.bfloat16, device=dev) if out_v is None else out_v
-    for n, t in (("out_k", out_k), ("out_v", out_v)):
-        _check_dev(n, t, torch.bfloat16, dev)
-        _check_out(n, t, (B, T, Hkv, d))
-    with _on_device(dev):
-        st = lib.fa_kv4_read(out_k.data_ptr(), out_v.data_ptr(), *(t.data_ptr() for t in cache), start.data_ptr(),
-                             _ptr(count), B, int(T), Hkv, Tk, d, _stream_ptr(dev))
-    _raise("fa_kv4_read", st)
+    index = _cuda_index("k_codes", cache[0])
+    B, Hkv, Tk, d = _cache_sizes(cache, index)
+    start_ptr, count_ptr = _counts(start, count, B, index)
+    shape = (B, T, Hkv, d)
+    kc, kp, vc, vp = cache
+    if out_k is None:
+        out_k = torch.empty(shape, dtype=torch.bfloat16, device=kc.device)
+    else:
+        _demand("out_k", out_k, torch.bfloat16, index, shape)
+    if out_v is None:
+        out_v = torch.empty(shape, dtype=torch.bfloat16, device=kc.device)
+    else:
+        _demand("out_v", out_v, torch.bfloat16, index, shape)
+    with _on_device(index):
+        st = lib.fa_kv4_read(out_k.data_ptr(), out_v.data_ptr(), kc.data_ptr(), kp.data_ptr(), vc.data_ptr(),
+                             vp.data_ptr(), start_ptr, count_ptr, B, T, Hkv, Tk, d, _stream_of(index))
+    if st:
+        _raise("fa_kv4_read", st)
     return out_k, out_v
 
 
@@ -128,30 +142,38 @@ def kv4_decode(q, cache, seqlens, scale=None, window=None, sinks=0, workspace=No
     of q [B,Hq,d] against the first seqlens[b] keys (int32 [B]) of each sequence;
     ``window`` and ``sinks`` as in decode_splitkv()."""
     lib = load_library()
-    if sinks and window is None:
-        raise ValueError("sinks need a window (without one every key is visible)")
-    if window is not None and window < 1:
+    if window is None:
+        if sinks:
+            raise ValueError("sinks need a window (without one every key is visible)")
+        window = 0
+    elif window < 1:
         raise ValueError(f"window must be at least 1, got {window}")
-    dev = q.device
-    _check_dev("q", q, torch.bfloat16, dev)
-    B, Hkv, Tk, d = _cache_sizes(cache, dev)
-    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d:
+    index = _cuda_index("q", q)
+    B, Hkv, Tk, d = _cache_sizes(cache, index)
+    if q.dim() != 3:
         raise ValueError(f"q must be [{B}, Hq, {d}], got {tuple(q.shape)}")
     Hq = q.shape[1]
-    _check_dev("seqlens", seqlens, torch.int32, dev)
-    if scale is None:
-        scale = d ** -0.5
-    need = kv4_decode_workspace_bytes(B, Hq, Hkv, Tk, d)
+    _demand("q", q, torch.bfloat16, index, (B, Hq, d))
+    _demand("seqlens", seqlens, torch.int32, index, (B,))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        need = lib.fa_kv4_decode_workspace_bytes(B, Hq, Hkv, Tk, d)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     else:
-        _check_dev("workspace", workspace, torch.uint8, dev)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=dev) if lse is None else lse
-    _check_decode_out(q, seqlens, out, lse)
-    with _on_device(dev):
-        st = lib.fa_kv4_decode(q.data_ptr(), *(t.data_ptr() for t in cache), seqlens.data_ptr(), out.data_ptr(),
-                               lse.data_ptr(), workspace.data_ptr(), workspace.numel(), B, Hq, Hkv, Tk, d,
-                               float(scale), 0 if window is None else int(window), int(sinks), _stream_ptr(dev))
-    _raise("fa_kv4_decode", st)
+        _check_dev("workspace", workspace, torch.uint8, q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _demand("out", out, torch.bfloat16, index, (B, Hq, d))
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _demand("lse", lse, torch.float32, index, (B, Hq))
+    kc, kp, vc, vp = cache
+    with _on_device(index):
+        st = lib.fa_kv4_decode(q.data_ptr(), kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(),
+                               seqlens.data_ptr(), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                               workspace.numel(), B, Hq, Hkv, Tk, d, d ** -0.5 if scale is None else scale, window,
+                               sinks, _stream_of(index))
+    if st:
+        _raise("fa_kv4_decode", st)
     return out, lse

@@ -17,7 +17,7 @@ import math
 
 import torch
 
-from ._binding import _check_dev, _on_device, _ptr, _raise, _stream_ptr, load_library
+from ._binding import _check_dev, _cuda_index, _demand, _on_device, _raise, _stream_of, load_library
 
 __all__ = ["rope_frequencies", "rope", "rope_backward"]
 
@@ -88,71 +88,64 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained
     return f.to(device) if device is not None else f, amplitude
 
 
-def _check_rows(name, t, dev, B, T, d):
+def _check_rows(name, t, index, B, T, d):
+    """(heads, batch, token and head stride) of bf16 [B,T,H,d] rows that are
+    contiguous in the last dim."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be on a CUDA device (libfa has no CPU path)")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype != torch.bfloat16:
+    if t.get_device() != index:
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be on a CUDA device (libfa has no CPU path)")
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != T or t.shape[3] != d:
-        raise ValueError(f"{name} must be [{B}, {T}, H, {d}], got {tuple(t.shape)}")
-    if t.stride(3) != 1:
+    shape, st = t.shape, t.stride()
+    if len(shape) != 4 or shape[0] != B or shape[1] != T or shape[3] != d:
+        raise ValueError(f"{name} must be [{B}, {T}, H, {d}], got {tuple(shape)}")
+    if st[3] != 1:
         raise ValueError(f"{name} must be contiguous in its last dim")
+    # no address depends on the stride of a dim of size 1
+    return shape[2], 0 if B == 1 else st[0], 0 if T == 1 else st[1], 0 if shape[2] == 1 else st[2]
 
 
 _STRIDES = ctypes.c_longlong * 12
 
 
-def _strides(*tensors):
-    """Batch, token and head strides, with those of dims of size 1 (which no
-    address depends on) as 0."""
-    st = []
-    for t in tensors:
-        for i in range(3):
-            st.append(0 if t is None or t.shape[i] == 1 else t.stride(i))
-    return _STRIDES(*st)
-
-
 def _rope(fn, q, k, freqs, positions, interleaved, amplitude, out_q, out_k):
     lib = load_library()
+    index = _cuda_index("q", q)
     if q.dim() != 4:
         raise ValueError(f"q must be [B, T, Hq, d], got {tuple(q.shape)}")
-    B, T, Hq, d = q.shape
-    dev = q.device
-    _check_rows("q", q, dev, B, T, d)
+    B, T, _, d = q.shape
+    Hq, *sq = _check_rows("q", q, index, B, T, d)
     if out_q is None:
-        out_q = torch.empty((B, T, Hq, d), dtype=torch.bfloat16, device=dev)
-    else:
-        _check_rows("out_q", out_q, dev, B, T, d)
-        if out_q.shape[2] != Hq:
-            raise ValueError(f"out_q must be {tuple(q.shape)}, got {tuple(out_q.shape)}")
-    Hkv = 0
+        out_q = torch.empty((B, T, Hq, d), dtype=torch.bfloat16, device=q.device)
+    h, *soq = _check_rows("out_q", out_q, index, B, T, d)
+    if h != Hq:
+        raise ValueError(f"out_q must be {tuple(q.shape)}, got {tuple(out_q.shape)}")
+    Hkv, kp, okp = 0, 0, 0
+    sk = sok = (0, 0, 0)
     if k is not None:
-        _check_rows("k", k, dev, B, T, d)
-        Hkv = k.shape[2]
+        Hkv, *sk = _check_rows("k", k, index, B, T, d)
         if out_k is None:
-            out_k = torch.empty((B, T, Hkv, d), dtype=torch.bfloat16, device=dev)
-        else:
-            _check_rows("out_k", out_k, dev, B, T, d)
-            if out_k.shape[2] != Hkv:
-                raise ValueError(f"out_k must be {tuple(k.shape)}, got {tuple(out_k.shape)}")
+            out_k = torch.empty((B, T, Hkv, d), dtype=torch.bfloat16, device=q.device)
+        h, *sok = _check_rows("out_k", out_k, index, B, T, d)
+        if h != Hkv:
+            raise ValueError(f"out_k must be {tuple(k.shape)}, got {tuple(out_k.shape)}")
+        kp, okp = k.data_ptr(), out_k.data_ptr()
     elif out_k is not None:
         raise ValueError("out_k without k")
-    _check_dev("freqs", freqs, torch.float64, dev)
     if freqs.dim() != 1:
         raise ValueError(f"freqs must be [rotary_dim / 2], got {tuple(freqs.shape)}")
+    _demand("freqs", freqs, torch.float64, index, freqs.shape)
     if positions is not None:
-        _check_dev("positions", positions, torch.int32, dev)
-        if tuple(positions.shape) != (B, T):
-            raise ValueError(f"positions must be {(B, T)}, got {tuple(positions.shape)}")
-    with _on_device(dev):
-        st = getattr(lib, fn)(q.data_ptr(), out_q.data_ptr(), _ptr(k), _ptr(out_k), _strides(q, out_q, k, out_k),
-                              _ptr(positions), freqs.data_ptr(), 2 * freqs.shape[0], int(bool(interleaved)),
-                              float(amplitude), B, T, Hq, Hkv, d, _stream_ptr(dev))
-    _raise(fn, st)
+        _demand("positions", positions, torch.int32, index, (B, T))
+    with _on_device(index):
+        st = getattr(lib, fn)(q.data_ptr(), out_q.data_ptr(), kp, okp, _STRIDES(*sq, *soq, *sk, *sok),
+                              0 if positions is None else positions.data_ptr(), freqs.data_ptr(), 2 * freqs.shape[0],
+                              1 if interleaved else 0, amplitude, B, T, Hq, Hkv, d, _stream_of(index))
+    if st:
+        _raise(fn, st)
     return out_q, out_k
 
 
