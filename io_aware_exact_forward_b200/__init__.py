@@ -33,4 +33,4 @@ from .kv4 import (  # noqa: F401,E402
     kv4_decode_workspace_bytes,
     kv4_read,
 )
-from .rope import rope, rope_backward, rope_frequencies  # noqa: F401,E402
+from .rotary import rope, rope_backward, rope_frequencies  # noqa: F401,E402

@@ -1139,10 +1139,12 @@ static int kv4_rows_blocks(Kv4RowsParams* p, int B, int T, int Hkv, int Tk_max, 
   p->T = T;
   p->H = Hkv;
   p->Tk_max = Tk_max;
-  const long long rows = (long long)B * T;
-  if (rows > (1ll << 40) / Hkv) return FA_ERR_INVALID_ARG;
-  p->units = rows * Hkv * (d / 8);
-  const long long n = (p->units + 255) / 256;
+  // a sequence's units are counted in 31 bits
+  const long long rows = (long long)T * Hkv;
+  if (rows > (1ll << 30) / (d / 8)) return FA_ERR_INVALID_ARG;
+  p->units = (unsigned)(rows * (d / 8));
+  p->blocks_per_seq = (p->units + 256 * kKv4Units - 1) / (256 * kKv4Units);
+  const long long n = (long long)B * p->blocks_per_seq;
   if (n > 0x7FFFFFFFll) return FA_ERR_INVALID_ARG;
   *blocks = (unsigned)n;
   return FA_OK;
@@ -1332,11 +1334,11 @@ extern "C" int fa_kv4_decode(const void* q, const void* k_codes, const void* k_p
     }
 #undef FA_KV4_LAUNCH
     if (st) return st;
-    const unsigned blocks = (unsigned)(((size_t)p.B * Hq * 32 + 255) / 256);
+    const unsigned blocks = (unsigned)(((size_t)p.B * Hq * 32 + 127) / 128);
     if (d == 64)
-      fa_kv4_combine_kernel<64><<<blocks, 256, 0, s>>>(p);
+      fa_kv4_combine_kernel<64><<<blocks, 128, 0, s>>>(p);
     else
-      fa_kv4_combine_kernel<128><<<blocks, 256, 0, s>>>(p);
+      fa_kv4_combine_kernel<128><<<blocks, 128, 0, s>>>(p);
     if ((st = launch_status())) return st;
   }
   return FA_OK;

@@ -128,6 +128,14 @@ __device__ __forceinline__ int chunk_keys(const DecodeParams& p, int k0, int seq
   return n;
 }
 
+// First 64-key tile of the chunk that holds a visible key: tiles before the
+// window are passed over, unless the chunk holds sinks.
+template <bool SINK>
+__device__ __forceinline__ int chunk_tile0(const DecodeParams& p, int k0, int seqlen) {
+  if (!SINK || k0 < p.sinks) return 0;
+  return max(0, seqlen - p.window - k0) / 64;
+}
+
 // Item k covers chunk k % nchunk of (sequence, KV head) k / nchunk; with SINK
 // the (k % nchunk)-th visible chunk, nchunk being the most that a sequence has.
 template <int D, int G, bool SINK = false>
@@ -189,6 +197,7 @@ fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
         const int k0 = c * p.chunk;
         if (!SINK && (k0 >= seqlen || (p.window > 0 && k0 + p.chunk <= seqlen - p.window))) continue;
         const int nsub = (chunk_keys<SINK>(p, k0, seqlen) + C::SUB - 1) / C::SUB;
+        const int i0 = chunk_tile0<SINK>(p, k0, seqlen);
         // the G query rows of the group are contiguous: one bulk copy
         const int qs = qi & 1;
         if (qi >= 2) ok = mbar_wait(bar_qempty(qs), ((qi >> 1) - 1) & 1, wc);
@@ -198,7 +207,7 @@ fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
                   bar_qfull(qs));
         ++qi;
         // K_0, V_0, K_1, V_1, ... -- the order the compute warps consume
-        for (int i = 0; i < 2 * nsub && ok; ++i, ++t) {
+        for (int i = 2 * i0; i < 2 * nsub && ok; ++i, ++t) {
           const int s = t % C::NSTAGE;
           const int round = t / C::NSTAGE;
           if (round > 0) ok = mbar_wait(bar_empty(s), (round - 1) & 1, wc);
@@ -272,7 +281,7 @@ fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) oacc[nb][e] = 0.f;
 
-    for (int i = 0; i < nsub; ++i) {
+    for (int i = chunk_tile0<SINK>(p, k0, seqlen); i < nsub; ++i) {
       // ---- K tile: scores of keys kw .. kw+15 of this 64-key tile
       const int sK = t % C::NSTAGE;
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_full(sK), (t / C::NSTAGE) & 1, wc));

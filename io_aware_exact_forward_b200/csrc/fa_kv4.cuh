@@ -31,7 +31,8 @@ struct Kv4RowsParams {
   __nv_bfloat16* params[2];
   const int* start;           // [B]: cache position of row t = 0
   const int* count;           // [B] rows of sequence b, or null: all T
-  long long units;            // B * T * H * (d / 8)
+  unsigned units;             // of 8 elements in one sequence: T * H * (d / 8)
+  unsigned blocks_per_seq;
   int T, H, Tk_max;
 };
 
@@ -46,64 +47,107 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Eight elements (16 bytes) of one row per thread; the four threads of a
-// group exchange its least and largest value by shuffles.  blockIdx.y = 0: K,
-// 1: V.
+// Both kernels below take units of eight elements of one row, kKv4Units of them
+// per thread, in the order (token, head, chunk) of one sequence; blockIdx.y = 0: K,
+// 1: V.  They are bound by HBM: 2 bytes an element on one side and 0.625 on the
+// other.  (With one index over the whole batch, divided in 64 bits, and a division
+// per element they took 110 and 56 us for 32k tokens of 8 heads of 128; the bytes
+// take 27.)
+static constexpr int kKv4Units = 2;
+
+struct Kv4Unit {
+  int ch, h, t;
+  bool in;
+  template <int CH>
+  __device__ __forceinline__ void at(const Kv4RowsParams& p, unsigned u) {
+    in = u < p.units;
+    if (!in) u = 0;
+    ch = (int)(u % CH);
+    const unsigned row = u / CH;
+    t = (int)(row / (unsigned)p.H);
+    h = (int)(row - (unsigned)t * (unsigned)p.H);
+  }
+};
+
+// round(t / s) + 8 of eight values, clamped to 0..15, as nibbles.  The quotient is
+// t inv + t inv_lo with inv + inv_lo = 1 / s to 48 bits: rounded once to fp32 it is
+// the division's own result (a quotient by an 8-bit s stays 2^-32 or more away from
+// where the rounding turns), ties of the code included, of which bf16 inputs have
+// many (a third of a percent of N(0,1) values).  Added to 1.5 2^23 + 8, the code is
+// the sum's low bits.
+__device__ __forceinline__ uint32_t kv4_codes(const float (&t)[8], float s) {
+  constexpr float M = 12582912.f;  // 1.5 2^23
+  uint32_t word = 0u;
+  if (s >= 0x1p-100f && s <= 0x1p100f) {
+    const float inv = __frcp_rn(s), inv_lo = fmaf(-s, inv, 1.f) * inv;
+#pragma unroll
+    for (int e = 7; e >= 0; --e) {
+      const float y = __fadd_rn(fmaf(t[e], inv, __fmul_rn(t[e], inv_lo)), M + 8.f);
+      word = word * 16u + (__float_as_uint(fminf(fmaxf(y, M), M + 15.f)) - 0x4B400000u);
+    }
+    return word;
+  }
+  if (!(s > 0.f)) return 0x88888888u;
+#pragma unroll 1
+  for (int e = 7; e >= 0; --e) {
+    const float c = fminf(fmaxf(rintf(__fdiv_rn(t[e], s)), -8.f), 7.f);
+    word = word * 16u + (uint32_t)((int)c + 8);
+  }
+  return word;
+}
+
+// The four threads of a group exchange its least and largest value by shuffles.
 template <int D>
 __global__ void __launch_bounds__(256) fa_kv4_append_kernel(const __grid_constant__ Kv4RowsParams p) {
   constexpr int CH = D / 8, NG = D / kKv4Group;
   const int which = blockIdx.y;
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const bool in = i < p.units;
-  const long long j = in ? i : 0;
-  const int ch = (int)(j % CH);
-  const long long row = j / CH;
-  const int h = (int)(row % p.H);
-  const long long bt = row / p.H;
-  const int t = (int)(bt % p.T);
-  const int b = (int)(bt / p.T);
-  const long long pos = (long long)p.start[b] + t;
-  const bool keep = in && t < (p.count ? p.count[b] : p.T) && pos >= 0 && pos < p.Tk_max;
-  const uint4 raw =
-      *reinterpret_cast<const uint4*>(p.x[which] + b * p.xb[which] + t * p.xt[which] + h * p.xh[which] + ch * 8);
-  const uint32_t* rw = reinterpret_cast<const uint32_t*>(&raw);
-  float x[8];
+  const int b = (int)(blockIdx.x / p.blocks_per_seq);
+  const unsigned u0 = (blockIdx.x - (unsigned)b * p.blocks_per_seq) * (256 * kKv4Units) + threadIdx.x;
+  const int start = p.start[b], count = p.count ? min(p.count[b], p.T) : p.T;
+  const __nv_bfloat16* xb = p.x[which] + b * p.xb[which];
+  Kv4Unit un[kKv4Units];
+  uint4 raw[kKv4Units];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&rw[e]));
-    x[2 * e] = f.x;
-    x[2 * e + 1] = f.y;
-  }
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int e = 1; e < 8; ++e) {
-    lo = min_nan(lo, x[e]);
-    hi = max_nan(hi, x[e]);
+  for (int n = 0; n < kKv4Units; ++n) {
+    un[n].at<CH>(p, u0 + 256 * n);
+    raw[n] = *reinterpret_cast<const uint4*>(xb + un[n].t * p.xt[which] + un[n].h * p.xh[which] + un[n].ch * 8);
   }
 #pragma unroll
-  for (int off = 1; off < 4; off <<= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-  }
-  const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(0.5f * hi, 0.5f * lo), 7.5f));
-  const float s = __bfloat162float(sb);
-  const __nv_bfloat16 zb = __float2bfloat16_rn(fmaf(8.f, s, lo));  // 8 s alone may overflow
-  const float z = __bfloat162float(zb);
-  uint32_t word = 0;
+  for (int n = 0; n < kKv4Units; ++n) {
+    const uint32_t rw[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+    float x[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float c = rintf(__fdiv_rn(__fsub_rn(x[e], z), s));
-    c = fminf(fmaxf(c, -8.f), 7.f);
-    const int code = s > 0.f ? (int)c + 8 : 8;
-    word |= (uint32_t)(code & 15) << (4 * e);
-  }
-  if (keep) {
-    const size_t r = ((size_t)b * p.H + h) * p.Tk_max + (size_t)pos;
-    *reinterpret_cast<uint32_t*>(p.codes[which] + r * (D / 2) + ch * 4) = word;
-    if ((ch & 3) == 0) {
-      __nv_bfloat16* pr = p.params[which] + r * (2 * NG) + (ch >> 2);
-      pr[0] = sb;
-      pr[NG] = zb;
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(rw[e] << 16);
+      x[2 * e + 1] = __uint_as_float(rw[e] & 0xFFFF0000u);
+    }
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) {
+      lo = min_nan(lo, x[e]);
+      hi = max_nan(hi, x[e]);
+    }
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    }
+    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(0.5f * hi, 0.5f * lo), 7.5f));
+    const float s = __bfloat162float(sb);
+    const __nv_bfloat16 zb = __float2bfloat16_rn(fmaf(8.f, s, lo));  // 8 s alone may overflow
+    const float z = __bfloat162float(zb);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __fsub_rn(x[e], z);
+    const uint32_t word = kv4_codes(x, s);
+    const long long pos = (long long)start + un[n].t;
+    if (un[n].in && un[n].t < count && pos >= 0 && pos < p.Tk_max) {
+      const size_t r = ((size_t)b * p.H + un[n].h) * p.Tk_max + (size_t)pos;
+      *reinterpret_cast<uint32_t*>(p.codes[which] + r * (D / 2) + un[n].ch * 4) = word;
+      if ((un[n].ch & 3) == 0) {
+        __nv_bfloat16* pr = p.params[which] + r * (2 * NG) + (un[n].ch >> 2);
+        pr[0] = sb;
+        pr[NG] = zb;
+      }
     }
   }
 }
@@ -114,31 +158,42 @@ template <int D>
 __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant__ Kv4RowsParams p) {
   constexpr int CH = D / 8, NG = D / kKv4Group;
   const int which = blockIdx.y;
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= p.units) return;
-  const int ch = (int)(i % CH);
-  const long long row = i / CH;
-  const int h = (int)(row % p.H);
-  const long long bt = row / p.H;
-  const int t = (int)(bt % p.T);
-  const int b = (int)(bt / p.T);
-  const long long pos = (long long)p.start[b] + t;
-  uint4 out = make_uint4(0u, 0u, 0u, 0u);
-  if (t < (p.count ? p.count[b] : p.T) && pos >= 0 && pos < p.Tk_max) {
-    const size_t r = ((size_t)b * p.H + h) * p.Tk_max + (size_t)pos;
-    const uint32_t word = *reinterpret_cast<const uint32_t*>(p.codes[which] + r * (D / 2) + ch * 4);
-    const __nv_bfloat16* pr = p.params[which] + r * (2 * NG) + (ch >> 2);
-    const float s = __bfloat162float(pr[0]), z = __bfloat162float(pr[NG]);
+  const int b = (int)(blockIdx.x / p.blocks_per_seq);
+  const unsigned u0 = (blockIdx.x - (unsigned)b * p.blocks_per_seq) * (256 * kKv4Units) + threadIdx.x;
+  const int start = p.start[b], count = p.count ? min(p.count[b], p.T) : p.T;
+  Kv4Unit un[kKv4Units];
+  uint32_t word[kKv4Units];
+  float s[kKv4Units], z[kKv4Units];
+#pragma unroll
+  for (int n = 0; n < kKv4Units; ++n) {
+    un[n].at<CH>(p, u0 + 256 * n);
+    const long long pos = (long long)start + un[n].t;
+    word[n] = 0x88888888u;  // zeros
+    s[n] = z[n] = 0.f;
+    if (un[n].t < count && pos >= 0 && pos < p.Tk_max) {
+      const size_t r = ((size_t)b * p.H + un[n].h) * p.Tk_max + (size_t)pos;
+      word[n] = *reinterpret_cast<const uint32_t*>(p.codes[which] + r * (D / 2) + un[n].ch * 4);
+      const __nv_bfloat16* pr = p.params[which] + r * (2 * NG) + (un[n].ch >> 2);
+      s[n] = __bfloat162float(pr[0]);
+      z[n] = __bfloat162float(pr[NG]);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < kKv4Units; ++n) {
+    if (!un[n].in) continue;
+    uint4 out;
     uint32_t* w = reinterpret_cast<uint32_t*>(&out);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float c0 = (float)((int)((word >> (8 * e)) & 15u) - 8);
-      const float c1 = (float)((int)((word >> (8 * e + 4)) & 15u) - 8);
-      // s (c - 8) is exact in 32 bits (8 by 4 bits), so one rounding each
-      w[e] = pack_bf16x2(fmaf(s, c0, z), fmaf(s, c1, z));
+      // u as the low bits of 2^23 + u; s (u - 8) is exact in 32 bits (8 by 4
+      // bits), so a value is rounded once to 32 bits and once to 16
+      const float c0 = __uint_as_float(0x4B000000u | ((word[n] >> (8 * e)) & 15u)) - 8388616.f;
+      const float c1 = __uint_as_float(0x4B000000u | ((word[n] >> (8 * e + 4)) & 15u)) - 8388616.f;
+      w[e] = pack_bf16x2(fmaf(s[n], c0, z[n]), fmaf(s[n], c1, z[n]));
     }
+    const size_t row = ((size_t)b * p.T + un[n].t) * p.H + un[n].h;
+    *reinterpret_cast<uint4*>(p.y[which] + row * D + un[n].ch * 8) = out;
   }
-  *reinterpret_cast<uint4*>(p.y[which] + row * D + ch * 8) = out;
 }
 
 // ---------------------------------------------------------------------------
@@ -720,37 +775,74 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
 }
 
 // One warp per (sequence, query head): the partial results of its stretch of
-// the list, joined.
+// the list, joined; eight of them in flight at a time.
 template <int D>
-__global__ void __launch_bounds__(256) fa_kv4_combine_kernel(const __grid_constant__ Kv4DecodeParams p) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(128) fa_kv4_combine_kernel(const __grid_constant__ Kv4DecodeParams p) {
+  constexpr int E = D / 32, U = 8;
   const int row = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   if (row >= p.B * p.Hq) return;
   const int G = p.Hq / p.Hkv;
   const int b = row / p.Hq, hkv = row % p.Hq / G, gq = row % G;
-  const long long total = (long long)p.ws_prefix[p.B] * p.Hkv;
-  const int count = p.ws_prefix[b + 1] - p.ws_prefix[b];
-  const int n_cta = (int)min((long long)p.n_cta, total);
-  __nv_bfloat16* dst = p.o + (size_t)row * D + lane * E;
+  const int before = p.ws_prefix[b], count = p.ws_prefix[b + 1] - before;
+  const int total = p.ws_prefix[p.B] * p.Hkv;
+  const int n_cta = min(p.n_cta, total);
   float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   if (count > 0) {
-    const long long first = (long long)p.ws_prefix[b] * p.Hkv + (long long)hkv * count;
+    const long long first = (long long)before * p.Hkv + (long long)hkv * count;
     // block i of tile t: the last with total * i / n <= t
     const int c0 = (int)(((first + 1) * n_cta - 1) / total), c1 = (int)(((first + count) * n_cta - 1) / total);
-    const size_t s0 = (size_t)b * p.Hkv + hkv;
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, p.ws_ml[((s0 + c) * G + gq) * 2]);
-    for (int c = c0; c <= c1; ++c) {
-      const size_t at = (s0 + c) * G + gq;
-      const float m = p.ws_ml[at * 2];
-      const float f = m == -INFINITY ? 0.f : ex2_approx(m - M);
-      L = fmaf(f, p.ws_ml[at * 2 + 1], L);
+    const size_t at0 = ((size_t)b * p.Hkv + hkv + c0) * G + gq;  // partial i at at0 + i * G
+    const int n = c1 - c0 + 1;
+    float m_own = -INFINITY, l_own = 0.f;  // partial `lane`
+    if (lane < n) {
+      const float2 ml = *reinterpret_cast<const float2*>(&p.ws_ml[(at0 + (size_t)lane * G) * 2]);
+      m_own = ml.x;
+      l_own = ml.y;
+    }
+    M = m_own;
+    for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, p.ws_ml[(at0 + (size_t)i * G) * 2]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(f, p.ws_o[at * D + lane * E + e], o[e]);
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    for (int i0 = 0; i0 < n; i0 += U) {
+      float f[U], v[U][E];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = min(i0 + u, n - 1);
+        const float* src = p.ws_o + (at0 + (size_t)i * G) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(src + e);
+          v[u][e] = x.x;
+          v[u][e + 1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u;
+        float m = -INFINITY, l = 0.f;
+        if (i0 + U <= 32) {
+          m = __shfl_sync(0xffffffffu, m_own, i & 31);
+          l = __shfl_sync(0xffffffffu, l_own, i & 31);
+        } else if (i < n) {
+          const float2 ml = *reinterpret_cast<const float2*>(&p.ws_ml[(at0 + (size_t)i * G) * 2]);
+          m = ml.x;
+          l = ml.y;
+        }
+        f[u] = i >= n || m == -INFINITY ? 0.f : ex2_approx(m - M);
+        if (i < n) L = fmaf(f[u], l, L);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u < n) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(f[u], v[u][e], o[e]);
+        }
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
+  __nv_bfloat16* dst = p.o + (size_t)row * D + lane * E;
 #pragma unroll
   for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
   if (lane == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;

@@ -118,11 +118,11 @@ def kv4_read(cache, start, T, count=None, out_k=None, out_v=None):
     shape = (B, T, Hkv, d)
     kc, kp, vc, vp = cache
     if out_k is None:
-        out_k = torch.empty(shape, dtype=torch.bfloat16, device=kc.device)
+        out_k = kp.new_empty(shape)
     else:
         _demand("out_k", out_k, torch.bfloat16, index, shape)
     if out_v is None:
-        out_v = torch.empty(shape, dtype=torch.bfloat16, device=kc.device)
+        out_v = kp.new_empty(shape)
     else:
         _demand("out_v", out_v, torch.bfloat16, index, shape)
     with _on_device(index):
@@ -157,7 +157,7 @@ def kv4_decode(q, cache, seqlens, scale=None, window=None, sinks=0, workspace=No
     _demand("seqlens", seqlens, torch.int32, index, (B,))
     if workspace is None:
         need = lib.fa_kv4_decode_workspace_bytes(B, Hq, Hkv, Tk, d)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = cache[0].new_empty(max(need, 16))
     else:
         _check_dev("workspace", workspace, torch.uint8, q.device)
     if out is None:

@@ -119,19 +119,23 @@ def _rope(fn, q, k, freqs, positions, interleaved, amplitude, out_q, out_k):
     B, T, _, d = q.shape
     Hq, *sq = _check_rows("q", q, index, B, T, d)
     if out_q is None:
-        out_q = torch.empty((B, T, Hq, d), dtype=torch.bfloat16, device=q.device)
-    h, *soq = _check_rows("out_q", out_q, index, B, T, d)
-    if h != Hq:
-        raise ValueError(f"out_q must be {tuple(q.shape)}, got {tuple(out_q.shape)}")
+        out_q = q.new_empty((B, T, Hq, d))
+        soq = T * Hq * d, Hq * d, d
+    else:
+        h, *soq = _check_rows("out_q", out_q, index, B, T, d)
+        if h != Hq:
+            raise ValueError(f"out_q must be {tuple(q.shape)}, got {tuple(out_q.shape)}")
     Hkv, kp, okp = 0, 0, 0
     sk = sok = (0, 0, 0)
     if k is not None:
         Hkv, *sk = _check_rows("k", k, index, B, T, d)
         if out_k is None:
-            out_k = torch.empty((B, T, Hkv, d), dtype=torch.bfloat16, device=q.device)
-        h, *sok = _check_rows("out_k", out_k, index, B, T, d)
-        if h != Hkv:
-            raise ValueError(f"out_k must be {tuple(k.shape)}, got {tuple(out_k.shape)}")
+            out_k = q.new_empty((B, T, Hkv, d))
+            sok = T * Hkv * d, Hkv * d, d
+        else:
+            h, *sok = _check_rows("out_k", out_k, index, B, T, d)
+            if h != Hkv:
+                raise ValueError(f"out_k must be {tuple(k.shape)}, got {tuple(out_k.shape)}")
         kp, okp = k.data_ptr(), out_k.data_ptr()
     elif out_k is not None:
         raise ValueError("out_k without k")
