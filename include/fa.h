@@ -462,7 +462,6 @@ int fa_rope_backward(const void* dq, void* dq_out, const void* dk, void* dk_out,
  *   start  DEVICE int32 [B];  count  DEVICE int32 [B], rows of sequence b that
  *          are written (t < count[b]), or NULL: all T.
  * Rows at positions outside [0, Tk_max) are dropped; nothing else is written.
- * T * Hkv * d at most 2^33.
  *
  * fa_kv4_read -- the values at positions start[b] + t, rounded to bf16, as dense
  * k, v [B,T,Hkv,d] (a prefill's keys, for instance).  Rows t >= count[b], or

@@ -1139,13 +1139,18 @@ static int kv4_rows_blocks(Kv4RowsParams* p, int B, int T, int Hkv, int Tk_max, 
   p->T = T;
   p->H = Hkv;
   p->Tk_max = Tk_max;
-  // a sequence's units are counted in 31 bits
-  const long long rows = (long long)T * Hkv;
-  if (rows > (1ll << 30) / (d / 8)) return FA_ERR_INVALID_ARG;
-  p->units = (unsigned)(rows * (d / 8));
-  p->blocks_per_seq = (p->units + 256 * kKv4Units - 1) / (256 * kKv4Units);
-  const long long n = (long long)B * p->blocks_per_seq;
+  // Eight steps along the tokens where that still leaves four blocks a
+  // multiprocessor, fewer where it does not.
+  if (Hkv > (1 << 24)) return FA_ERR_INVALID_ARG;
+  p->heads = Hkv >= 2 ? 2 : 1;
+  p->parts = (Hkv + p->heads - 1) / p->heads;
+  p->tokens = 256 / (p->heads * (d / 8));
+  p->steps = 1;
+  while (p->steps < 8 && (long long)B * (T / (p->tokens * p->steps * 2)) * p->parts >= 4 * 148) p->steps *= 2;
+  const long long per_seq = (((long long)T + p->tokens * p->steps - 1) / (p->tokens * p->steps)) * p->parts;
+  const long long n = per_seq * B;
   if (n > 0x7FFFFFFFll) return FA_ERR_INVALID_ARG;
+  p->blocks_per_seq = (unsigned)per_seq;
   *blocks = (unsigned)n;
   return FA_OK;
 }

@@ -31,9 +31,11 @@ struct Kv4RowsParams {
   __nv_bfloat16* params[2];
   const int* start;           // [B]: cache position of row t = 0
   const int* count;           // [B] rows of sequence b, or null: all T
-  unsigned units;             // of 8 elements in one sequence: T * H * (d / 8)
-  unsigned blocks_per_seq;
   int T, H, Tk_max;
+  // a block: `heads` heads (one of `parts` such groups) of `tokens` tokens side by
+  // side, `steps` times along the tokens
+  unsigned blocks_per_seq;
+  int heads, tokens, parts, steps;
 };
 
 __device__ __forceinline__ float min_nan(float a, float b) {
@@ -47,53 +49,101 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Both kernels below take units of eight elements of one row, kKv4Units of them
-// per thread, in the order (token, head, chunk) of one sequence; blockIdx.y = 0: K,
-// 1: V.  They are bound by HBM: 2 bytes an element on one side and 0.625 on the
-// other.  (With one index over the whole batch, divided in 64 bits, and a division
-// per element they took 110 and 56 us for 32k tokens of 8 heads of 128; the bytes
-// take 27.)
-static constexpr int kKv4Units = 2;
-
-struct Kv4Unit {
-  int ch, h, t;
-  bool in;
-  template <int CH>
-  __device__ __forceinline__ void at(const Kv4RowsParams& p, unsigned u) {
-    in = u < p.units;
-    if (!in) u = 0;
-    ch = (int)(u % CH);
-    const unsigned row = u / CH;
-    t = (int)(row / (unsigned)p.H);
-    h = (int)(row - (unsigned)t * (unsigned)p.H);
+// The two constants of the conversions, in registers that the compiler cannot
+// see through: as literals, the mask and the OR are two instructions (an
+// instruction takes one literal), not one.
+struct Kv4Const {
+  uint32_t magic, m136;  // bf16 pairs (128, 128) and (136, 136)
+  __device__ __forceinline__ Kv4Const() {
+    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(magic));
+    asm volatile("mov.b32 %0, 0x43084308;" : "=r"(m136));
+  }
+  // Nibble k of both halves as the bf16 pair 128 + u.
+  __device__ __forceinline__ uint32_t pair(uint32_t w, int k) const {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(r) : "r"(w >> (4 * k)), "r"(magic));
+    return r;
+  }
+  // The same as u - 8.
+  __device__ __forceinline__ uint32_t pair_c(uint32_t w, int k) const {
+    const uint32_t u = pair(w, k);
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&m136));
+    return *reinterpret_cast<const uint32_t*>(&r);
   }
 };
 
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Both kernels below take units of eight elements of one row.  A thread keeps its
+// head and its place in the row and walks along the tokens, so that indexes are
+// divided out once; a block has two heads of 8 tokens (d = 128; 16 at 64) side by
+// side, so that it meets 512 contiguous bytes on either side at a time.  They are bound by HBM (2 bytes an element on one side and
+// 0.625 on the other) and, closely behind, by issue: 32k tokens of 8 heads of 128
+// take the bytes 27 us each way.  One index per unit divided out in 64 bits and a
+// division per element took 110 and 56 us, in 32 bits without the divisions 64 and
+// 45.
+struct Kv4Place {
+  int b, h, ch, t;  // sequence, head, unit of the row, first token
+  bool in;
+  template <int CH>
+  static __device__ __forceinline__ Kv4Place of(const Kv4RowsParams& p) {
+    Kv4Place w;
+    w.b = (int)(blockIdx.x / p.blocks_per_seq);
+    const unsigned r = blockIdx.x - (unsigned)w.b * p.blocks_per_seq;
+    const unsigned tb = r / (unsigned)p.parts, part = r - tb * (unsigned)p.parts;
+    const unsigned row = threadIdx.x / CH;
+    const unsigned tl = p.heads == 2 ? row >> 1 : row;
+    w.ch = (int)(threadIdx.x % CH);
+    w.h = (int)(part * p.heads + (row - tl * p.heads));
+    w.in = w.h < p.H;
+    if (!w.in) w.h = 0;
+    w.t = (int)(tb * (unsigned)(p.tokens * p.steps) + tl);
+    return w;
+  }
+};
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // round(t / s) + 8 of eight values, clamped to 0..15, as nibbles.  The quotient is
-// t inv + t inv_lo with inv + inv_lo = 1 / s to 48 bits: rounded once to fp32 it is
+// t inv + t inv_lo with inv + inv_lo = 1 / s to 45 bits: rounded once to fp32 it is
 // the division's own result (a quotient by an 8-bit s stays 2^-32 or more away from
 // where the rounding turns), ties of the code included, of which bf16 inputs have
 // many (a third of a percent of N(0,1) values).  Added to 1.5 2^23 + 8, the code is
 // the sum's low bits.
-__device__ __forceinline__ uint32_t kv4_codes(const float (&t)[8], float s) {
+__device__ __forceinline__ uint32_t kv4_codes(const float2 (&t)[4], float s) {
   constexpr float M = 12582912.f;  // 1.5 2^23
   uint32_t word = 0u;
   if (s >= 0x1p-100f && s <= 0x1p100f) {
-    const float inv = __frcp_rn(s), inv_lo = fmaf(-s, inv, 1.f) * inv;
+    const float inv = rcp_approx(s), inv_lo = fmaf(-s, inv, 1.f) * inv;
+    const float2 i2 = make_float2(inv, inv), l2 = make_float2(inv_lo, inv_lo), m2 = make_float2(M + 8.f, M + 8.f);
 #pragma unroll
-    for (int e = 7; e >= 0; --e) {
-      const float y = __fadd_rn(fmaf(t[e], inv, __fmul_rn(t[e], inv_lo)), M + 8.f);
-      word = word * 16u + (__float_as_uint(fminf(fmaxf(y, M), M + 15.f)) - 0x4B400000u);
+    for (int e = 3; e >= 0; --e) {
+      const float2 y = __fadd2_rn(__ffma2_rn(t[e], i2, __fmul2_rn(t[e], l2)), m2);
+      word = word * 16u + __float_as_uint(fminf(fmaxf(y.y, M), M + 15.f));
+      word = word * 16u + __float_as_uint(fminf(fmaxf(y.x, M), M + 15.f));
     }
-    return word;
+    return word - 0x4B400000u * 0x11111111u;  // M's own bits, eight times over
   }
   if (!(s > 0.f)) return 0x88888888u;
 #pragma unroll 1
   for (int e = 7; e >= 0; --e) {
-    const float c = fminf(fmaxf(rintf(__fdiv_rn(t[e], s)), -8.f), 7.f);
+    const float c = fminf(fmaxf(rintf(__fdiv_rn(e & 1 ? t[e >> 1].y : t[e >> 1].x, s)), -8.f), 7.f);
     word = word * 16u + (uint32_t)((int)c + 8);
   }
   return word;
+}
+
+// x / 7.5, rounded once: x times 1 / 7.5 in two parts, as above.
+__device__ __forceinline__ float div_7_5(float x) {
+  constexpr float inv = 1.f / 7.5f, inv_lo = (float)(1.0 / 7.5 - (double)inv);
+  if (x >= 0x1p-90f && x <= 0x1p127f) return fmaf(x, inv, __fmul_rn(x, inv_lo));
+  return __fdiv_rn(x, 7.5f);
 }
 
 // The four threads of a group exchange its least and largest value by shuffles.
@@ -101,50 +151,42 @@ template <int D>
 __global__ void __launch_bounds__(256) fa_kv4_append_kernel(const __grid_constant__ Kv4RowsParams p) {
   constexpr int CH = D / 8, NG = D / kKv4Group;
   const int which = blockIdx.y;
-  const int b = (int)(blockIdx.x / p.blocks_per_seq);
-  const unsigned u0 = (blockIdx.x - (unsigned)b * p.blocks_per_seq) * (256 * kKv4Units) + threadIdx.x;
-  const int start = p.start[b], count = p.count ? min(p.count[b], p.T) : p.T;
-  const __nv_bfloat16* xb = p.x[which] + b * p.xb[which];
-  Kv4Unit un[kKv4Units];
-  uint4 raw[kKv4Units];
-#pragma unroll
-  for (int n = 0; n < kKv4Units; ++n) {
-    un[n].at<CH>(p, u0 + 256 * n);
-    raw[n] = *reinterpret_cast<const uint4*>(xb + un[n].t * p.xt[which] + un[n].h * p.xh[which] + un[n].ch * 8);
-  }
-#pragma unroll
-  for (int n = 0; n < kKv4Units; ++n) {
-    const uint32_t rw[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = __uint_as_float(rw[e] << 16);
-      x[2 * e + 1] = __uint_as_float(rw[e] & 0xFFFF0000u);
-    }
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) {
-      lo = min_nan(lo, x[e]);
-      hi = max_nan(hi, x[e]);
-    }
+  const Kv4Place w = Kv4Place::of<CH>(p);
+  const int start = p.start[w.b], count = p.count ? min(p.count[w.b], p.T) : p.T;
+  const __nv_bfloat16* x = p.x[which] + w.b * p.xb[which] + w.h * p.xh[which] + w.ch * 8;
+  const size_t row0 = ((size_t)w.b * p.H + w.h) * p.Tk_max;
+  uint8_t* codes = p.codes[which] + row0 * (D / 2) + w.ch * 4;
+  __nv_bfloat16* params = p.params[which] + row0 * (2 * NG) + (w.ch >> 2);
+  const long long xt = p.xt[which];
+#pragma unroll 2
+  for (int n = 0; n < p.steps; ++n) {
+    const int t = w.t + n * p.tokens;
+    // every thread takes part in the shuffles; one past the end reads row 0
+    const uint4 raw = *reinterpret_cast<const uint4*>(x + (w.in && t < p.T ? t : 0) * xt);
+    const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
+    auto pair = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    auto bits = [](__nv_bfloat162 w) { return *reinterpret_cast<const uint32_t*>(&w); };
+    uint32_t lo2 = bits(__hmin2_nan(__hmin2_nan(pair(rw[0]), pair(rw[1])), __hmin2_nan(pair(rw[2]), pair(rw[3]))));
+    uint32_t hi2 = bits(__hmax2_nan(__hmax2_nan(pair(rw[0]), pair(rw[1])), __hmax2_nan(pair(rw[2]), pair(rw[3]))));
 #pragma unroll
     for (int off = 1; off < 4; off <<= 1) {
-      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+      lo2 = bits(__hmin2_nan(pair(lo2), pair(__shfl_xor_sync(0xffffffffu, lo2, off))));
+      hi2 = bits(__hmax2_nan(pair(hi2), pair(__shfl_xor_sync(0xffffffffu, hi2, off))));
     }
-    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(0.5f * hi, 0.5f * lo), 7.5f));
+    const float lo = min_nan(bf16_lo(lo2), bf16_hi(lo2)), hi = max_nan(bf16_lo(hi2), bf16_hi(hi2));
+    const __nv_bfloat16 sb = __float2bfloat16_rn(div_7_5(__fsub_rn(0.5f * hi, 0.5f * lo)));
     const float s = __bfloat162float(sb);
     const __nv_bfloat16 zb = __float2bfloat16_rn(fmaf(8.f, s, lo));  // 8 s alone may overflow
     const float z = __bfloat162float(zb);
+    float2 v[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __fsub_rn(x[e], z);
-    const uint32_t word = kv4_codes(x, s);
-    const long long pos = (long long)start + un[n].t;
-    if (un[n].in && un[n].t < count && pos >= 0 && pos < p.Tk_max) {
-      const size_t r = ((size_t)b * p.H + un[n].h) * p.Tk_max + (size_t)pos;
-      *reinterpret_cast<uint32_t*>(p.codes[which] + r * (D / 2) + un[n].ch * 4) = word;
-      if ((un[n].ch & 3) == 0) {
-        __nv_bfloat16* pr = p.params[which] + r * (2 * NG) + (un[n].ch >> 2);
+    for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(make_float2(bf16_lo(rw[e]), bf16_hi(rw[e])), make_float2(-z, -z));
+    const uint32_t word = kv4_codes(v, s);
+    const long long pos = (long long)start + t;
+    if (w.in && t < count && pos >= 0 && pos < p.Tk_max) {
+      *reinterpret_cast<uint32_t*>(codes + (size_t)pos * (D / 2)) = word;
+      if ((w.ch & 3) == 0) {
+        __nv_bfloat16* pr = params + (size_t)pos * (2 * NG);
         pr[0] = sb;
         pr[NG] = zb;
       }
@@ -158,41 +200,38 @@ template <int D>
 __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant__ Kv4RowsParams p) {
   constexpr int CH = D / 8, NG = D / kKv4Group;
   const int which = blockIdx.y;
-  const int b = (int)(blockIdx.x / p.blocks_per_seq);
-  const unsigned u0 = (blockIdx.x - (unsigned)b * p.blocks_per_seq) * (256 * kKv4Units) + threadIdx.x;
-  const int start = p.start[b], count = p.count ? min(p.count[b], p.T) : p.T;
-  Kv4Unit un[kKv4Units];
-  uint32_t word[kKv4Units];
-  float s[kKv4Units], z[kKv4Units];
-#pragma unroll
-  for (int n = 0; n < kKv4Units; ++n) {
-    un[n].at<CH>(p, u0 + 256 * n);
-    const long long pos = (long long)start + un[n].t;
-    word[n] = 0x88888888u;  // zeros
-    s[n] = z[n] = 0.f;
-    if (un[n].t < count && pos >= 0 && pos < p.Tk_max) {
-      const size_t r = ((size_t)b * p.H + un[n].h) * p.Tk_max + (size_t)pos;
-      word[n] = *reinterpret_cast<const uint32_t*>(p.codes[which] + r * (D / 2) + un[n].ch * 4);
-      const __nv_bfloat16* pr = p.params[which] + r * (2 * NG) + (un[n].ch >> 2);
-      s[n] = __bfloat162float(pr[0]);
-      z[n] = __bfloat162float(pr[NG]);
+  const Kv4Place w = Kv4Place::of<CH>(p);
+  if (!w.in) return;
+  const Kv4Const kc4;
+  const int start = p.start[w.b], count = p.count ? min(p.count[w.b], p.T) : p.T;
+  const size_t row0 = ((size_t)w.b * p.H + w.h) * p.Tk_max;
+  const uint8_t* codes = p.codes[which] + row0 * (D / 2) + w.ch * 4;
+  const __nv_bfloat16* params = p.params[which] + row0 * (2 * NG) + (w.ch >> 2);
+  __nv_bfloat16* y = p.y[which] + ((size_t)w.b * p.T * p.H + w.h) * D + w.ch * 8;
+#pragma unroll 4
+  for (int n = 0; n < p.steps; ++n) {
+    const int t = w.t + n * p.tokens;
+    if (t >= p.T) break;
+    const long long pos = (long long)start + t;
+    uint32_t word = 0x88888888u;  // zeros
+    __nv_bfloat162 s = __float2bfloat162_rn(0.f), z = s;
+    if (t < count && pos >= 0 && pos < p.Tk_max) {
+      word = *reinterpret_cast<const uint32_t*>(codes + (size_t)pos * (D / 2));
+      const __nv_bfloat16* pr = params + (size_t)pos * (2 * NG);
+      s = __halves2bfloat162(pr[0], pr[0]);
+      z = __halves2bfloat162(pr[NG], pr[NG]);
     }
-  }
+    // pairs (k, k + 4) of the row: s (u - 8) + z in one fused, once rounded step
+    uint32_t q[4];
 #pragma unroll
-  for (int n = 0; n < kKv4Units; ++n) {
-    if (!un[n].in) continue;
-    uint4 out;
-    uint32_t* w = reinterpret_cast<uint32_t*>(&out);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // u as the low bits of 2^23 + u; s (u - 8) is exact in 32 bits (8 by 4
-      // bits), so a value is rounded once to 32 bits and once to 16
-      const float c0 = __uint_as_float(0x4B000000u | ((word[n] >> (8 * e)) & 15u)) - 8388616.f;
-      const float c1 = __uint_as_float(0x4B000000u | ((word[n] >> (8 * e + 4)) & 15u)) - 8388616.f;
-      w[e] = pack_bf16x2(fmaf(s[n], c0, z[n]), fmaf(s[n], c1, z[n]));
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t u = kc4.pair_c(word, k);
+      const __nv_bfloat162 x = __hfma2(s, *reinterpret_cast<const __nv_bfloat162*>(&u), z);
+      q[k] = *reinterpret_cast<const uint32_t*>(&x);
     }
-    const size_t row = ((size_t)b * p.T + un[n].t) * p.H + un[n].h;
-    *reinterpret_cast<uint4*>(p.y[which] + row * D + un[n].ch * 8) = out;
+    const uint4 out = make_uint4(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
+                                 __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632));
+    *reinterpret_cast<uint4*>(y + (size_t)t * p.H * D) = out;
   }
 }
 
@@ -300,33 +339,6 @@ __device__ __forceinline__ uint32_t kv4_swz(int r, int c) {
   if constexpr (D == 128) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
   return (uint32_t)(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
 }
-
-// The two constants of the conversions, in registers that the compiler cannot
-// see through: as literals, the mask and the OR are two instructions (an
-// instruction takes one literal), not one.
-struct Kv4Const {
-  uint32_t magic, m136;  // bf16 pairs (128, 128) and (136, 136)
-  __device__ __forceinline__ Kv4Const() {
-    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(magic));
-    asm volatile("mov.b32 %0, 0x43084308;" : "=r"(m136));
-  }
-  // Nibble k of both halves as the bf16 pair 128 + u.
-  __device__ __forceinline__ uint32_t pair(uint32_t w, int k) const {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(r) : "r"(w >> (4 * k)), "r"(magic));
-    return r;
-  }
-  // The same as u - 8.
-  __device__ __forceinline__ uint32_t pair_c(uint32_t w, int k) const {
-    const uint32_t u = pair(w, k);
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&m136));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-};
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t r;
