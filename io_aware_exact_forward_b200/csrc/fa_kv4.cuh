@@ -131,7 +131,7 @@ __device__ __forceinline__ uint32_t kv4_codes(const float2 (&t)[4], float s) {
     return word - 0x4B400000u * 0x11111111u;  // M's own bits, eight times over
   }
   if (!(s > 0.f)) return 0x88888888u;
-#pragma unroll 1
+#pragma unroll
   for (int e = 7; e >= 0; --e) {
     const float c = fminf(fmaxf(rintf(__fdiv_rn(e & 1 ? t[e >> 1].y : t[e >> 1].x, s)), -8.f), 7.f);
     word = word * 16u + (uint32_t)((int)c + 8);
@@ -156,14 +156,22 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(const __grid_constan
   const __nv_bfloat16* x = p.x[which] + w.b * p.xb[which] + w.h * p.xh[which] + w.ch * 8;
   const size_t row0 = ((size_t)w.b * p.H + w.h) * p.Tk_max;
   uint8_t* codes = p.codes[which] + row0 * (D / 2) + w.ch * 4;
-  __nv_bfloat16* params = p.params[which] + row0 * (2 * NG) + (w.ch >> 2);
+  __nv_bfloat16* params = p.params[which] + row0 * (2 * NG);
   const long long xt = p.xt[which];
-#pragma unroll 2
-  for (int n = 0; n < p.steps; ++n) {
-    const int t = w.t + n * p.tokens;
-    // every thread takes part in the shuffles; one past the end reads row 0
-    const uint4 raw = *reinterpret_cast<const uint4*>(x + (w.in && t < p.T ? t : 0) * xt);
-    const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
+  constexpr int U = 4;  // loads in flight
+  for (int n0 = 0; n0 < p.steps; n0 += U) {
+   uint4 raw[U];
+#pragma unroll
+   for (int u = 0; u < U; ++u) {
+     // every thread takes part in the shuffles; one past the end reads row 0
+     const int t = w.t + (n0 + u) * p.tokens;
+     raw[u] = *reinterpret_cast<const uint4*>(x + (w.in && n0 + u < p.steps && t < p.T ? t : 0) * xt);
+   }
+#pragma unroll
+   for (int u = 0; u < U; ++u) {
+    if (n0 + u >= p.steps) break;
+    const int t = w.t + (n0 + u) * p.tokens;
+    const uint32_t rw[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
     auto pair = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
     auto bits = [](__nv_bfloat162 w) { return *reinterpret_cast<const uint32_t*>(&w); };
     uint32_t lo2 = bits(__hmin2_nan(__hmin2_nan(pair(rw[0]), pair(rw[1])), __hmin2_nan(pair(rw[2]), pair(rw[3]))));
@@ -182,15 +190,29 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(const __grid_constan
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(make_float2(bf16_lo(rw[e]), bf16_hi(rw[e])), make_float2(-z, -z));
     const uint32_t word = kv4_codes(v, s);
+    // the row's steps and centres at its first thread, for one store
+    const __nv_bfloat162 sz = __halves2bfloat162(sb, zb);
+    const uint32_t w0 = bits(sz);
+    const uint32_t w1 = __shfl_down_sync(0xffffffffu, w0, 4, CH);
+    uint32_t w2 = 0u, w3 = 0u;
+    if constexpr (NG == 4) {
+      w2 = __shfl_down_sync(0xffffffffu, w0, 8, CH);
+      w3 = __shfl_down_sync(0xffffffffu, w0, 12, CH);
+    }
     const long long pos = (long long)start + t;
     if (w.in && t < count && pos >= 0 && pos < p.Tk_max) {
       *reinterpret_cast<uint32_t*>(codes + (size_t)pos * (D / 2)) = word;
-      if ((w.ch & 3) == 0) {
+      if (w.ch == 0) {
+        const uint32_t s01 = __byte_perm(w0, w1, 0x5410), z01 = __byte_perm(w0, w1, 0x7632);
         __nv_bfloat16* pr = params + (size_t)pos * (2 * NG);
-        pr[0] = sb;
-        pr[NG] = zb;
+        if constexpr (NG == 4)
+          *reinterpret_cast<uint4*>(pr) = make_uint4(s01, __byte_perm(w2, w3, 0x5410), z01,
+                                                     __byte_perm(w2, w3, 0x7632));
+        else
+          *reinterpret_cast<uint2*>(pr) = make_uint2(s01, z01);
       }
     }
+   }
   }
 }
 
@@ -208,30 +230,40 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
   const uint8_t* codes = p.codes[which] + row0 * (D / 2) + w.ch * 4;
   const __nv_bfloat16* params = p.params[which] + row0 * (2 * NG) + (w.ch >> 2);
   __nv_bfloat16* y = p.y[which] + ((size_t)w.b * p.T * p.H + w.h) * D + w.ch * 8;
-#pragma unroll 4
-  for (int n = 0; n < p.steps; ++n) {
-    const int t = w.t + n * p.tokens;
-    if (t >= p.T) break;
-    const long long pos = (long long)start + t;
-    uint32_t word = 0x88888888u;  // zeros
-    __nv_bfloat162 s = __float2bfloat162_rn(0.f), z = s;
-    if (t < count && pos >= 0 && pos < p.Tk_max) {
-      word = *reinterpret_cast<const uint32_t*>(codes + (size_t)pos * (D / 2));
-      const __nv_bfloat16* pr = params + (size_t)pos * (2 * NG);
-      s = __halves2bfloat162(pr[0], pr[0]);
-      z = __halves2bfloat162(pr[NG], pr[NG]);
-    }
-    // pairs (k, k + 4) of the row: s (u - 8) + z in one fused, once rounded step
-    uint32_t q[4];
+  constexpr int U = 4;  // loads in flight
+  for (int n = 0; n < p.steps; n += U) {
+    uint32_t word[U];
+    __nv_bfloat16 s[U], z[U];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t u = kc4.pair_c(word, k);
-      const __nv_bfloat162 x = __hfma2(s, *reinterpret_cast<const __nv_bfloat162*>(&u), z);
-      q[k] = *reinterpret_cast<const uint32_t*>(&x);
+    for (int u = 0; u < U; ++u) {
+      const int t = w.t + (n + u) * p.tokens;
+      const long long pos = (long long)start + t;
+      word[u] = 0x88888888u;  // zeros
+      s[u] = z[u] = __float2bfloat16_rn(0.f);
+      if (n + u < p.steps && t < count && pos >= 0 && pos < p.Tk_max) {
+        word[u] = *reinterpret_cast<const uint32_t*>(codes + (size_t)pos * (D / 2));
+        const __nv_bfloat16* pr = params + (size_t)pos * (2 * NG);
+        s[u] = pr[0];
+        z[u] = pr[NG];
+      }
     }
-    const uint4 out = make_uint4(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
-                                 __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632));
-    *reinterpret_cast<uint4*>(y + (size_t)t * p.H * D) = out;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = w.t + (n + u) * p.tokens;
+      // pairs (k, k + 4) of the row: s (u - 8) + z in one fused, once rounded step
+      uint32_t q[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t c = kc4.pair_c(word[u], k);
+        const __nv_bfloat162 x = __hfma2(__halves2bfloat162(s[u], s[u]), *reinterpret_cast<const __nv_bfloat162*>(&c),
+                                         __halves2bfloat162(z[u], z[u]));
+        q[k] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+      if (n + u < p.steps && t < p.T)
+        *reinterpret_cast<uint4*>(y + (size_t)t * p.H * D) =
+            make_uint4(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
+                       __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632));
+    }
   }
 }
 
