@@ -519,7 +519,7 @@ static int dkdv_impl(const void* q, const void* k, const void* v, const void* dO
   // dK and dV of cut-up sink tiles, once their pieces are done
   auto sum_sinks = [&]() -> int {
     if (sinks == 0 || p.pieces == 1) return FA_OK;
-    const dim3 g((unsigned)(B * Hkv * p.n_sink_tiles), 2);
+    const dim3 g((unsigned)(B * Hkv * p.n_sink_tiles * (d / 8)), 2);
     if (d == 64)
       fa_bwd_sink_sum_kernel<64><<<g, 256, 0, s>>>(p.sink_part, p.dk, p.dv, Hkv, Tk, p.n_sink_tiles, p.pieces);
     else

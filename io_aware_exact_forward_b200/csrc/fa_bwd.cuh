@@ -1050,30 +1050,32 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
 }
 
 // dK and dV of the sink tiles from their pieces, summed in the pieces' order.
-// One thread per four elements: grid (slots of 128 keys, [dV, dK]).
+// One thread per four elements, 1024 elements a block: grid (slots of 128 keys x
+// D / 8, [dV, dK]).
 template <int D>
 __global__ void __launch_bounds__(256) fa_bwd_sink_sum_kernel(const float* __restrict__ part,
                                                               __nv_bfloat16* __restrict__ dk,
                                                               __nv_bfloat16* __restrict__ dv, int Hkv, int Tk,
                                                               int n_sink_tiles, int pieces) {
-  const int kt = blockIdx.x % n_sink_tiles, hb = blockIdx.x / n_sink_tiles, which = blockIdx.y;
-  for (int i = threadIdx.x; i < 128 * D / 4; i += blockDim.x) {
-    const int j = i / (D / 4), c = i % (D / 4);
-    const int key = kt * 128 + j;
-    if (key >= Tk) continue;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int n = 0; n < pieces; ++n) {
-      const float4 x = *reinterpret_cast<const float4*>(
-          part + ((((size_t)blockIdx.x * pieces + n) * 2 + which) * 128 + j) * D + c * 4);
-      a.x += x.x;
-      a.y += x.y;
-      a.z += x.z;
-      a.w += x.w;
-    }
-    const size_t row = ((size_t)(hb / Hkv) * Tk + key) * Hkv + hb % Hkv;
-    *reinterpret_cast<uint2*>((which ? dk : dv) + row * D + c * 4) =
-        make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  const int slot = blockIdx.x / (D / 8), which = blockIdx.y;
+  const int kt = slot % n_sink_tiles, hb = slot / n_sink_tiles;
+  const int i = (blockIdx.x % (D / 8)) * 256 + threadIdx.x;
+  const int j = i / (D / 4), c = i % (D / 4);
+  const int key = kt * 128 + j;
+  if (key >= Tk) return;
+  const float4* src = reinterpret_cast<const float4*>(part + (((size_t)slot * pieces * 2 + which) * 128 + j) * D) + c;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int n = 0; n < pieces; ++n) {
+    const float4 x = src[(size_t)n * (2 * 128 * D / 4)];
+    a.x += x.x;
+    a.y += x.y;
+    a.z += x.z;
+    a.w += x.w;
   }
+  const size_t row = ((size_t)(hb / Hkv) * Tk + key) * Hkv + hb % Hkv;
+  *reinterpret_cast<uint2*>((which ? dk : dv) + row * D + c * 4) =
+      make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
 }
 
 static int bwd_setup() {

@@ -157,6 +157,13 @@ struct FwdCfg {
   static_assert(!F8 || D == 128, "the E4M3 forward is built for d = 128");
 };
 
+// Bits 0 .. n - 1 (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  uint32_t r;  // shl by 32 gives 0
+  asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(0xFFFFFFFFu), "r"(min(max(n, 0), 32)));
+  return ~r;
+}
+
 // One work item: two query tiles [m0, m0 + 256) of head h of batch b,
 // against KV tiles kv0 .. kv0 + n_kv - 1; with sinks the first n_sink of the
 // n_kv tiles are tiles 0 .. n_sink - 1 and kv0 is the first tile after them.
@@ -588,12 +595,22 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, DROP>::THREADS, 1) fa_fwd_kernel
         const int nvalid = key_limit - fwd_kv_tile<SINK>(it, j) * C::BN;  // columns >= nvalid are masked
         const int nlo = key_lo - fwd_kv_tile<SINK>(it, j) * C::BN;         // and columns < nlo
         const bool masked = __any_sync(0xffffffffu, nvalid < C::BN || nlo > 0);
-        if (masked) {
-          // columns below nsk are sinks: masked by the causal edge alone
-          const int nsk = SINK ? p.sinks - fwd_kv_tile<SINK>(it, j) * C::BN : 0;
+        if (SINK && masked) {
+          // Columns below nsk are sinks: masked by the causal edge alone.  The
+          // three bounds as one bit per column: two instructions a column, not
+          // four, on the most of a short window's tiles.
+          const int nsk = p.sinks - fwd_kv_tile<SINK>(it, j) * C::BN;
+#pragma unroll
+          for (int w4 = 0; w4 < 4; ++w4) {
+            const uint32_t m = bits_below(nvalid - 32 * w4) & (~bits_below(nlo - 32 * w4) | bits_below(nsk - 32 * w4));
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(m & (1u << c))) su[32 * w4 + c] = __float_as_uint(-INFINITY);
+          }
+        } else if (masked) {
 #pragma unroll
           for (int c = 0; c < 128; ++c)
-            if (c >= nvalid || (c < nlo && (!SINK || c >= nsk))) su[c] = __float_as_uint(-INFINITY);
+            if (c >= nvalid || c < nlo) su[c] = __float_as_uint(-INFINITY);
         }
         // Row maximum: eight independent chains of three-input maxima (two
         // new columns per step), then a short tree.
