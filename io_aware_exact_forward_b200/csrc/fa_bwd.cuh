@@ -743,6 +743,13 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
           if (key < p.sinks) cmax = 1 << 30;  // a sink stays visible
         }
         const bool masked = __any_sync(0xffffffffu, !key_ok || cmin > 0 || (WIN && cmax < 64));
+        uint32_t seen[2] = {0u, 0u};  // sinks: bit per column, as most tiles of a short window are masked
+        if constexpr (WIN == 2) {
+          if (key_ok) {
+            seen[0] = bits_below(cmax) & ~bits_below(cmin);
+            seen[1] = bits_below(cmax - 32) & ~bits_below(cmin - 32);
+          }
+        }
         // 64 query columns in four 16-column chunks; the load of chunk c+1
         // overlaps the exponentials of chunk c.  P^T (bf16 pairs) goes to
         // the first 32 columns of this warp's 64, never ahead of its loads.
@@ -763,7 +770,10 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
                                         sl2, make_float2(-l2.x, -l2.y));
             float p0 = ex2_approx(x.x);
             float p1 = ex2_approx(x.y);
-            if (masked) {
+            if (WIN == 2 && masked) {
+              if (!(seen[col >> 5] & (1u << (col & 31)))) p0 = 0.f;
+              if (!(seen[col >> 5] & (2u << (col & 31)))) p1 = 0.f;
+            } else if (masked) {
               if (!key_ok || col < cmin || (WIN && col >= cmax)) p0 = 0.f;
               if (!key_ok || col + 1 < cmin || (WIN && col + 1 >= cmax)) p1 = 0.f;
             }

@@ -296,17 +296,25 @@ __global__ void __launch_bounds__(320, 1) fa_bwd_dq_kernel(const __grid_constant
       const int kbase = dq_kv_tile<WIN>(it, j) * 128 + 64 * hc;
       const int nvalid = key_limit - kbase;  // columns >= nvalid are masked
       const int nlo = key_lo - kbase;        // and columns < nlo
-      // columns below nsk are sinks: masked by the causal edge alone
-      const int nsk = WIN == 2 ? p.sinks - kbase : 0;
       const bool masked = __any_sync(0xffffffffu, nvalid < 64 || (WIN && nlo > 0));
+      uint32_t seen[2] = {0u, 0u};  // sinks: bit per column
+      if constexpr (WIN == 2) {
+        const int nsk = p.sinks - kbase;  // columns below are sinks: masked by the causal edge alone
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          seen[i] = bits_below(nvalid - 32 * i) & (~bits_below(nlo - 32 * i) | bits_below(nsk - 32 * i));
+      }
       uint32_t ds[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), sl2, nl2);
         float2 pr = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-        if (masked) {
-          if (2 * e >= nvalid || (WIN && 2 * e < nlo && (WIN != 2 || 2 * e >= nsk))) pr.x = 0.f;
-          if (2 * e + 1 >= nvalid || (WIN && 2 * e + 1 < nlo && (WIN != 2 || 2 * e + 1 >= nsk))) pr.y = 0.f;
+        if (WIN == 2 && masked) {
+          if (!(seen[e >> 4] & (1u << ((2 * e) & 31)))) pr.x = 0.f;
+          if (!(seen[e >> 4] & (2u << ((2 * e) & 31)))) pr.y = 0.f;
+        } else if (masked) {
+          if (2 * e >= nvalid || (WIN && 2 * e < nlo)) pr.x = 0.f;
+          if (2 * e + 1 >= nvalid || (WIN && 2 * e + 1 < nlo)) pr.y = 0.f;
         }
         const float2 t = __fadd2_rn(make_float2(__uint_as_float(dv[2 * e]), __uint_as_float(dv[2 * e + 1])), ndd);
         const float2 g = __fmul2_rn(pr, t);

@@ -157,13 +157,6 @@ struct FwdCfg {
   static_assert(!F8 || D == 128, "the E4M3 forward is built for d = 128");
 };
 
-// Bits 0 .. n - 1 (none for n <= 0, all for n >= 32).
-__device__ __forceinline__ uint32_t bits_below(int n) {
-  uint32_t r;  // shl by 32 gives 0
-  asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(0xFFFFFFFFu), "r"(min(max(n, 0), 32)));
-  return ~r;
-}
-
 // One work item: two query tiles [m0, m0 + 256) of head h of batch b,
 // against KV tiles kv0 .. kv0 + n_kv - 1; with sinks the first n_sink of the
 // n_kv tiles are tiles 0 .. n_sink - 1 and kv0 is the first tile after them.
