@@ -505,7 +505,9 @@ static int dkdv_impl(const void* q, const void* k, const void* v, const void* dO
   // length and the hardware scheduler balances them.
   int nsm = 0;
   if ((st = sm_count(&nsm))) return st;
-  const bool persistent = d == 64 && !causal;
+  // With sinks the items are alike by construction (the sink tiles' pieces are
+  // as long as a windowed item) and, in a short window, only a few tiles long.
+  const bool persistent = d == 64 && (!causal || sinks > 0);
   dim3 grid(persistent ? std::min(p.n_items, nsm) : p.n_items);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (drop && (window > 0 || det)) return FA_ERR_UNSUPPORTED;

@@ -588,7 +588,13 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
           issue_dp(0, kvb);
           started = true;
         }
-        const bool has_next_item = item + (int)gridDim.x < p.n_items;
+        bool has_next_item = item + (int)gridDim.x < p.n_items;
+        if constexpr (WIN == 2 && D == 64) {
+          // a persistent block: items that no query sees are passed over
+          int n = item + (int)gridDim.x;
+          while (n < p.n_items && bwd_item<WIN>(p, n).n_it == 0) n += gridDim.x;
+          has_next_item = n < p.n_items;
+        }
         for (int it = 0; it < I.n_it && ok; ++it, ++gi) {
           const int buf = gi % C::NSBUF;
           const bool last = it + 1 == I.n_it;

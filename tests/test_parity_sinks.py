@@ -64,6 +64,27 @@ def test_sink_backward(B, Hq, Hkv, Tq, Tk, d, W, S, deterministic):
         assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+@pytest.mark.parametrize("deterministic", [False, True])
+@pytest.mark.parametrize("B,Hq,Hkv,Tq,Tk,d,W,S", [
+    (2, 32, 32, 300, 700, 64, 40, 3),         # key tiles that no query sees among a block's items
+    (3, 20, 20, 520, 520, 64, 130, 140),
+    (2, 40, 20, 640, 640, 128, 60, 5),
+])
+def test_sink_backward_many_items(B, Hq, Hkv, Tq, Tk, d, W, S, deterministic):
+    """More work items than multiprocessors: blocks walk several."""
+    q, k, v, do = _inputs(B, Hq, Hkv, Tq, Tk, d, W, S)
+    c = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.forward(*c[:3], window=W, sinks=S)
+    got = fa.backward(*c[:3], o, lse, c[3], window=W, sinks=S, deterministic=deterministic)
+    assert fa.check() == 0
+    fo, ft, fl = P.sink_forward(q, k, v, W, S, d ** -0.5)
+    P.check(o, fo, ft, "O")
+    P.check_lse(lse, fl)
+    ref = P.sink_backward(q, k, v, do, W, S, d ** -0.5)
+    for n, x in zip(("dq", "dk", "dv"), got):
+        P.check(x, *ref[n], n)
+
+
 def test_sink_gradient_against_differences():
     """Directional derivatives of L = sum(dO * O): the 64-bit loss's central
     difference along u against the kernel's gradients."""
