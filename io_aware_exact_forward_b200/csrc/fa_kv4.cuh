@@ -54,9 +54,24 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // instruction takes one literal), not one.
 struct Kv4Const {
   uint32_t magic, m136;  // bf16 pairs (128, 128) and (136, 136)
+  uint32_t h1024, h1032, h16, h72;  // fp16 pairs 1024, -1032, 1 / 16, -72
   __device__ __forceinline__ Kv4Const() {
     asm volatile("mov.b32 %0, 0x43004300;" : "=r"(magic));
     asm volatile("mov.b32 %0, 0x43084308;" : "=r"(m136));
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(h1024));
+    asm volatile("mov.b32 %0, 0xE408E408;" : "=r"(h1032));
+    asm volatile("mov.b32 %0, 0x2C002C00;" : "=r"(h16));
+    asm volatile("mov.b32 %0, 0xD480D480;" : "=r"(h72));
+  }
+  // Nibbles 0 and 1 of both halves as the fp16 pairs u - 8 (a word shifted by 8
+  // gives 2 and 3): the nibble ORed into 1024 at its place, 1024 + u or
+  // 1024 + 16 u, then one exact fp16 step.
+  __device__ __forceinline__ void pair_h(uint32_t w, uint32_t& lo, uint32_t& hi) const {
+    uint32_t a, b;
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(a) : "r"(w), "r"(h1024));
+    asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(b) : "r"(w), "r"(h1024));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(h1032));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(hi) : "r"(b), "r"(h16), "r"(h72));
   }
   // Nibble k of both halves as the bf16 pair 128 + u.
   __device__ __forceinline__ uint32_t pair(uint32_t w, int k) const {
@@ -389,6 +404,23 @@ __device__ __forceinline__ void mma_1688_z(float (&d)[4], uint32_t a0, uint32_t 
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
+// D = A B (C = 0) and D += A B in fp16.
+__device__ __forceinline__ void mma_f16_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 // D = A B + C with C apart from D, so that a constant C stays in its registers.
 __device__ __forceinline__ void mma_16816_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
@@ -552,25 +584,47 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
     // has, hold the next group's Q rather than zeros, so that every operand is
     // four registers that stay)
     uint32_t qa[NG][4];
-    float qinit[NG][2];   // -136 sum of the group's q, twice: the accumulator's two columns
+    float qscale;            // what the row's products are multiplied by
     uint32_t za0, za1 = 0u;  // sum q: parts 0 and 1 in row g, part 2 in row g + 8
     {
       const __nv_bfloat16* qrow = p.q + ((size_t)sg.pair * G + (g < G ? g : 0)) * D;
+      uint4 v[NG];
+      float amax = 0.f;
+#pragma unroll
+      for (int c = 0; c < NG; ++c) {
+        v[c] = *reinterpret_cast<const uint4*>(qrow + 32 * c + 8 * t4);
+        if (g >= G) v[c] = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) amax = max_nan(amax, max_nan(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+      }
+      amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // 2^-e brings the row's largest value into [2^14, 2^15) (less below 2^-98);
+      // a row with a NaN, an infinity or anything from 2^118 on, whose scores
+      // would leave fp32, gives NaN
+      const int e = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -112);
+      const bool fine = amax < 0x1p118f;
+      const float down = fine ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
+      qscale = fine ? __uint_as_float((uint32_t)(127 + e) << 23) * p.scale_log2 : NAN;
       float qs[NG];
 #pragma unroll
       for (int c = 0; c < NG; ++c) {
-        uint4 v = *reinterpret_cast<const uint4*>(qrow + 32 * c + 8 * t4);
-        if (g >= G) v = make_uint4(0u, 0u, 0u, 0u);
-        qa[c][0] = __byte_perm(v.x, v.z, 0x5410);
-        qa[c][1] = __byte_perm(v.x, v.z, 0x7632);
-        qa[c][2] = __byte_perm(v.y, v.w, 0x5410);
-        qa[c][3] = __byte_perm(v.y, v.w, 0x7632);
-        float q8 = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) +
-                   ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
+        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        float q8 = 0.f;
+        float2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = make_float2(bf16_lo(w[i]) * down, bf16_hi(w[i]) * down);
+          q8 += x[i].x + x[i].y;
+        }
+        qa[c][0] = pack_f16x2(x[0].x, x[2].x);  // dims 8t, 8t + 4
+        qa[c][1] = pack_f16x2(x[0].y, x[2].y);
+        qa[c][2] = pack_f16x2(x[1].x, x[3].x);
+        qa[c][3] = pack_f16x2(x[1].y, x[3].y);
         q8 += __shfl_xor_sync(0xffffffffu, q8, 1);
         q8 += __shfl_xor_sync(0xffffffffu, q8, 2);
         qs[c] = q8;
-        qinit[c][0] = qinit[c][1] = -136.f * q8;
       }
       // sum q of every group in three bf16 parts: columns (part, group) of the
       // row operand that meets the centres
@@ -657,16 +711,19 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
             // group c in the accumulator's rows 0..7, group c + 1 in the other's 8..15
             float x[4], y[4];
             const uint32_t w0 = kc[nb][c], w1 = kc[nb][c + 1];
-            mma_16816_c(x, qa[c][0], qa[c + 1][0], qa[c][1], qa[c + 1][1], kc4.pair(w0, 0), kc4.pair(w0, 1),
-                        qinit[c][0], qinit[c][1], qinit[c + 1][0], qinit[c + 1][1]);
-            mma_16816_c(y, qa[c][0], qa[c + 1][0], qa[c][1], qa[c + 1][1], kc4.pair(w1, 0), kc4.pair(w1, 1),
-                        qinit[c][0], qinit[c][1], qinit[c + 1][0], qinit[c + 1][1]);
-            mma_16816(x, qa[c][2], qa[c + 1][2], qa[c][3], qa[c + 1][3], kc4.pair(w0, 2), kc4.pair(w0, 3));
-            mma_16816(y, qa[c][2], qa[c + 1][2], qa[c][3], qa[c + 1][3], kc4.pair(w1, 2), kc4.pair(w1, 3));
+            uint32_t b0, b1;
+            kc4.pair_h(w0, b0, b1);
+            mma_f16_z(x, qa[c][0], qa[c + 1][0], qa[c][1], qa[c + 1][1], b0, b1);
+            kc4.pair_h(w1, b0, b1);
+            mma_f16_z(y, qa[c][0], qa[c + 1][0], qa[c][1], qa[c + 1][1], b0, b1);
+            kc4.pair_h(w0 >> 8, b0, b1);
+            mma_f16(x, qa[c][2], qa[c + 1][2], qa[c][3], qa[c + 1][3], b0, b1);
+            kc4.pair_h(w1 >> 8, b0, b1);
+            mma_f16(y, qa[c][2], qa[c + 1][2], qa[c][3], qa[c + 1][3], b0, b1);
             tot = __ffma2_rn(make_float2(bf16_lo(s0[c / 2]), bf16_lo(s1[c / 2])), make_float2(x[0], x[1]), tot);
             tot = __ffma2_rn(make_float2(bf16_hi(s0[c / 2]), bf16_hi(s1[c / 2])), make_float2(y[2], y[3]), tot);
           }
-          sc[u][nb] = __fmul2_rn(tot, make_float2(p.scale_log2, p.scale_log2));
+          sc[u][nb] = __fmul2_rn(tot, make_float2(qscale, qscale));
         }
       }
       if (!whole) {
