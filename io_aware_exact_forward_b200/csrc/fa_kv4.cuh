@@ -49,42 +49,38 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// The two constants of the conversions, in registers that the compiler cannot
-// see through: as literals, the mask and the OR are two instructions (an
-// instruction takes one literal), not one.
-struct Kv4Const {
-  uint32_t magic, m136;  // bf16 pairs (128, 128) and (136, 136)
-  uint32_t h1024, h1032, h16, h72;  // fp16 pairs 1024, -1032, 1 / 16, -72
-  __device__ __forceinline__ Kv4Const() {
-    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(magic));
+// The constants of the conversions are in registers that the compiler cannot see
+// through: as literals, the mask and the OR are two instructions (an instruction
+// takes one literal), not one.
+struct Kv4PairsBf16 {
+  uint32_t m128, m136;  // pairs of 128 and 136
+  __device__ __forceinline__ Kv4PairsBf16() {
+    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(m128));
     asm volatile("mov.b32 %0, 0x43084308;" : "=r"(m136));
+  }
+  // Nibble k of both halves as the bf16 pair u - 8: ORed into 128, less 136.
+  __device__ __forceinline__ __nv_bfloat162 pair(uint32_t w, int k) const {
+    uint32_t u;
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(u) : "r"(w >> (4 * k)), "r"(m128));
+    return __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&m136));
+  }
+};
+struct Kv4PairsF16 {
+  uint32_t h1024, h1032, h16, h72;  // pairs of 1024, -1032, 1 / 16, -72
+  __device__ __forceinline__ Kv4PairsF16() {
     asm volatile("mov.b32 %0, 0x64006400;" : "=r"(h1024));
     asm volatile("mov.b32 %0, 0xE408E408;" : "=r"(h1032));
     asm volatile("mov.b32 %0, 0x2C002C00;" : "=r"(h16));
     asm volatile("mov.b32 %0, 0xD480D480;" : "=r"(h72));
   }
-  // Nibbles 0 and 1 of both halves as the fp16 pairs u - 8 (a word shifted by 8
-  // gives 2 and 3): the nibble ORed into 1024 at its place, 1024 + u or
-  // 1024 + 16 u, then one exact fp16 step.
-  __device__ __forceinline__ void pair_h(uint32_t w, uint32_t& lo, uint32_t& hi) const {
+  // Nibbles 0 and 1 of both halves as the fp16 pairs u - 8 (of the word shifted
+  // by 8: nibbles 2 and 3), from 1024 + u and 1024 + 16 u.
+  __device__ __forceinline__ void pairs(uint32_t w, uint32_t& n0, uint32_t& n1) const {
     uint32_t a, b;
     asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(a) : "r"(w), "r"(h1024));
     asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(b) : "r"(w), "r"(h1024));
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(h1032));
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(hi) : "r"(b), "r"(h16), "r"(h72));
-  }
-  // Nibble k of both halves as the bf16 pair 128 + u.
-  __device__ __forceinline__ uint32_t pair(uint32_t w, int k) const {
-    uint32_t r;
-    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(r) : "r"(w >> (4 * k)), "r"(magic));
-    return r;
-  }
-  // The same as u - 8.
-  __device__ __forceinline__ uint32_t pair_c(uint32_t w, int k) const {
-    const uint32_t u = pair(w, k);
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&m136));
-    return *reinterpret_cast<const uint32_t*>(&r);
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(n0) : "r"(a), "r"(h1032));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(n1) : "r"(b), "r"(h16), "r"(h72));
   }
 };
 
@@ -239,7 +235,7 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
   const int which = blockIdx.y;
   const Kv4Place w = Kv4Place::of<CH>(p);
   if (!w.in) return;
-  const Kv4Const kc4;
+  const Kv4PairsBf16 bf;
   const int start = p.start[w.b], count = p.count ? min(p.count[w.b], p.T) : p.T;
   const size_t row0 = ((size_t)w.b * p.H + w.h) * p.Tk_max;
   const uint8_t* codes = p.codes[which] + row0 * (D / 2) + w.ch * 4;
@@ -269,9 +265,8 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
       uint32_t q[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t c = kc4.pair_c(word[u], k);
-        const __nv_bfloat162 x = __hfma2(__halves2bfloat162(s[u], s[u]), *reinterpret_cast<const __nv_bfloat162*>(&c),
-                                         __halves2bfloat162(z[u], z[u]));
+        const __nv_bfloat162 x =
+            __hfma2(__halves2bfloat162(s[u], s[u]), bf.pair(word[u], k), __halves2bfloat162(z[u], z[u]));
         q[k] = *reinterpret_cast<const uint32_t*>(&x);
       }
       if (n + u < p.steps && t < p.T)
@@ -291,16 +286,26 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
 // so the steps never touch the d codes of a row: they scale 32-bit sums of four
 // group products of a score, and the probabilities on the way into P V.
 //
-// On the tensor cores (mma.sync m16n8k16; a decode has too few rows for a
-// tcgen05 tile) a code enters K's product as the bf16 128 + u, which is a mask
-// and an OR of its nibble, exact, with no conversion; the 136 = 128 + 8 is taken
-// off by starting the score's accumulator at -136 sum q.  V's codes enter as
-// u - 8, one more (exact) bf16 subtraction: taking 136 sum p s off O's sums
-// instead loses what averaging over a long sequence leaves of O (measured 0.9%
-// of O's norm at 17k keys, against 0.2%).  The centres' parts are two small
-// products of their own: z against sum q (split into three bf16 parts, 24
-// bits), and p against z.  p s is formed in 32 bits and rounded to bf16 once; l
-// sums the unrounded p.
+// On the tensor cores (mma.sync m16n8k16: a decode has too few rows for a
+// tcgen05 tile) the codes are the fp16 numbers u - 8, without a conversion: a
+// nibble masked and ORed into 1024, where it stands (1024 + u, or 1024 + 16 u), is
+// brought to u - 8 by one exact fp16 addition or fused multiply-add, so that a
+// 32-bit word of eight codes takes one shift.  (bf16 holds one nibble of every
+// four, hence three shifts; the shifts and masks go through the half-rate integer
+// pipe, which with the instruction issue is what bounds this kernel after HBM.)
+// Q enters as fp16 after scaling its row by a power of two to a largest value in
+// [2^14, 2^15): a bf16 value is then exact down to 2^-31 of the row's largest, and
+// smaller ones are within 2^-39 of it.  The centres' parts are two small bf16
+// products of their own: z against sum q (in three bf16 parts, 24 bits), and p
+// against z.
+//
+// p s is formed in 32 bits and rounded to fp16 once (2^-12 of itself); l sums the
+// unrounded p.  fp16's range: p carries a power of two that brings the largest
+// step so far to 2^3 .. 2^4, lowered when a step eight times as large comes (then
+// the sums so far are rescaled, as for a moved maximum).  A p s that is 2^18 below
+// that loses bits and one 2^28 below it is dropped: that is p itself, or a key
+// whose steps are that much smaller than others that the same warp has met.  Steps
+// below 2^-70 or from 2^107 on leave fp16's range altogether.
 //
 // Operand layouts.  A 16-byte chunk of a row's codes is one group.  For K,
 // ldmatrix gives lane (g, t) of a warp the word of key g's dims 8t .. 8t + 7 of
@@ -421,14 +426,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// D = A B + C with C apart from D, so that a constant C stays in its registers.
-__device__ __forceinline__ void mma_16816_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                            uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+// Whether either of a bf16 pair is above its limit (NaN is not).
+__device__ __forceinline__ bool bf16x2_any_gt(uint32_t x, uint32_t lim) {
+  uint32_t r;
+  asm("{\n\t.reg .pred p, q;\n\tsetp.gt.bf16x2 p|q, %1, %2;\n\tor.pred p, p, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(x), "r"(lim));
+  return r != 0;
 }
 
 // The steps of one row's params, as words of two.
@@ -536,7 +540,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
   int left = (int)((long long)total * (blockIdx.x + 1) / n_cta) - at;
 
   const int g = lane >> 2, t4 = lane & 3;
-  const Kv4Const kc4;
+  const Kv4PairsF16 codes16;
   bool ok = true;
   uint32_t phases = 0;  // bit s: parity of the next use of stage s
 
@@ -649,6 +653,11 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
     }
 
     float m_run = -INFINITY, l_part = 0.f;   // row g
+    // p carries a factor 2^lv that places p s in fp16's range: the steps seen so
+    // far are at most 2^(7 - lv), and p s at most 2^15.  `step_limit` is that bound
+    // as a bf16 pair.
+    float lv = 0.f;
+    uint32_t step_limit = 0u;
     float oacc[NG][2][4];                    // dims 32c + 4g + 2kk (+1), queries 2t, 2t + 1
     float zacc[4] = {0.f, 0.f, 0.f, 0.f};    // sum of p z, by group
 #pragma unroll
@@ -712,13 +721,13 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
             float x[4], y[4];
             const uint32_t w0 = kc[nb][c], w1 = kc[nb][c + 1];
             uint32_t b0, b1;
-            kc4.pair_h(w0, b0, b1);
+            codes16.pairs(w0, b0, b1);
             mma_f16_z(x, qa[c][0], qa[c + 1][0], qa[c][1], qa[c + 1][1], b0, b1);
-            kc4.pair_h(w1, b0, b1);
+            codes16.pairs(w1, b0, b1);
             mma_f16_z(y, qa[c][0], qa[c + 1][0], qa[c][1], qa[c + 1][1], b0, b1);
-            kc4.pair_h(w0 >> 8, b0, b1);
+            codes16.pairs(w0 >> 8, b0, b1);
             mma_f16(x, qa[c][2], qa[c + 1][2], qa[c][3], qa[c + 1][3], b0, b1);
-            kc4.pair_h(w1 >> 8, b0, b1);
+            codes16.pairs(w1 >> 8, b0, b1);
             mma_f16(y, qa[c][2], qa[c + 1][2], qa[c][3], qa[c + 1][3], b0, b1);
             tot = __ffma2_rn(make_float2(bf16_lo(s0[c / 2]), bf16_lo(s1[c / 2])), make_float2(x[0], x[1]), tot);
             tot = __ffma2_rn(make_float2(bf16_hi(s0[c / 2]), bf16_hi(s1[c / 2])), make_float2(y[2], y[3]), tot);
@@ -741,13 +750,26 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const bool move = mx > m_run + C::RESCALE_THRESHOLD || (m_run == -INFINITY && mx != -INFINITY);
-      if (__any_sync(0xffffffffu, move)) {
-        float alpha = 1.f;
-        if (move) {
-          alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - mx);
-          m_run = mx;
-          l_part *= alpha;
-        }
+      uint32_t sw[NG / 2];  // the steps of key `lane`
+      kv4_steps<NG>(st + C::OFF_VP + lane * C::PB, sw);
+      bool wide = bf16x2_any_gt(sw[0], step_limit);
+      if constexpr (NG == 4) wide |= bf16x2_any_gt(sw[1], step_limit);
+      if (__any_sync(0xffffffffu, move || wide)) {
+        float smax = fmaxf(bf16_lo(sw[0]), bf16_hi(sw[0]));
+        if constexpr (NG == 4) smax = fmaxf(smax, fmaxf(bf16_lo(sw[1]), bf16_hi(sw[1])));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, off));
+        // 2^lv brings the largest step into [2^3, 2^4), which leaves room for steps
+        // eight times as large
+        const float fit = (float)min(max(130 - (int)(__float_as_uint(smax) >> 23), -100), 60);
+        const float lv_new = step_limit == 0u ? fit : fminf(lv, fit);
+        float alpha = 0.f;
+        if (m_run != -INFINITY) alpha = ex2_approx((m_run - lv) - ((move ? mx : m_run) - lv_new));
+        if (move) m_run = mx;
+        lv = lv_new;
+        step_limit = (uint32_t)(127 + 7 - (int)lv) << 7;
+        step_limit |= step_limit << 16;
+        l_part *= alpha;
         const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t4);      // row 2t
         const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);  // row 2t + 1
 #pragma unroll
@@ -759,7 +781,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) zacc[e] *= (e & 1) ? a1 : a0;
       }
-      const float ref = m_run == -INFINITY ? 0.f : m_run;
+      const float ref = m_run == -INFINITY ? 0.f : m_run - lv;
       float2 pv[2][2];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -804,11 +826,14 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
             const float2 f1 = cc ? make_float2(bf16_hi(sv[2][c2 / 2]), bf16_hi(sv[3][c2 / 2]))
                                  : make_float2(bf16_lo(sv[2][c2 / 2]), bf16_lo(sv[3][c2 / 2]));
             const float2 p0 = __fmul2_rn(pv[u][0], f0), p1 = __fmul2_rn(pv[u][1], f1);
-            const uint32_t b0 = pack_bf16x2(p0.x, p0.y), b1 = pack_bf16x2(p1.x, p1.y);
+            const uint32_t b0 = pack_f16x2(p0.x, p0.y), b1 = pack_f16x2(p1.x, p1.y);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              mma_16816(oacc[c][k], kc4.pair_c(vc[cc][0], 2 * k), kc4.pair_c(vc[cc][0], 2 * k + 1),
-                        kc4.pair_c(vc[cc][1], 2 * k), kc4.pair_c(vc[cc][1], 2 * k + 1), b0, b1);
+            for (int k = 0; k < 2; ++k) {
+              uint32_t v0, v1, v2, v3;
+              codes16.pairs(vc[cc][0] >> (8 * k), v0, v1);
+              codes16.pairs(vc[cc][1] >> (8 * k), v2, v3);
+              mma_f16(oacc[c][k], v0, v1, v2, v3, b0, b1);
+            }
           }
         }
       }
@@ -829,7 +854,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
     float l_row = l_part + __shfl_xor_sync(0xffffffffu, l_part, 1);
     l_row += __shfl_xor_sync(0xffffffffu, l_row, 2);
     if (t4 == 0) {
-      m_s[warp * 8 + g] = m_run;
+      m_s[warp * 8 + g] = m_run - lv;
       l_s[warp * 8 + g] = l_row;
     }
 #pragma unroll

@@ -141,6 +141,48 @@ def test_decode(Hq, Hkv, d, Tk, W, S, seqlens):
     assert torch.equal(o, o2) and torch.equal(lse, lse2), "the same inputs give the same bits"
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scales", [
+    [1e-6], [1e4], [3e4, 1.0], [1e-3, 1e3],       # per third of the sequence, values of V
+    [1.0, 300.0, 1e5], [1e5, 300.0, 1.0], [1e-12, 1e-9, 1e-10],
+])
+def test_decode_value_ranges(d, scales):
+    """Values of other sizes, growing and falling along the sequence: the
+    probabilities' scaling follows them."""
+    Hkv, Hq, Tk = 2, 8, 704
+    k = _rand((1, Hkv, Tk, d), 90)
+    f = torch.tensor([scales[min(len(scales) - 1, 3 * i // Tk * len(scales) // 3)] for i in range(Tk)])
+    v = (_rand((1, Hkv, Tk, d), 91).float() * f[:, None]).to(torch.bfloat16)
+    cache = fa.KV4Cache(*(t.cuda() for x in (k, v) for t in P.pack4(x)))
+    q = (_rand((1, Hq, d), 92).float() * 2).to(torch.bfloat16)
+    o, lse = fa.kv4_decode(q.cuda(), cache, _i32([700]))
+    assert fa.check() == 0
+    vv, vp = P.values4(cache.v_codes, cache.v_params)
+    ref, tol, rl = P.decode(q, P.values4(cache.k_codes, cache.k_params)[0], vv, vp, [700], 0, 0, d ** -0.5)
+    P.check(o, ref, tol, "O")
+    P.check_lse(lse, rl)
+
+
+def test_decode_query_ranges():
+    """Rows of q of very different sizes, zero, and with a NaN or an infinity."""
+    cache, (kv, _), (vv, vp) = _filled(1, 1, 128, 128, 95)
+    q = _rand((1, 8, 128), 96).float()
+    q[0, 1] *= 1e-20
+    q[0, 2] = 0
+    q[0, 3] *= torch.logspace(0, -12, 128)      # 40 binades within a row
+    q[0, 4, 7] = float("nan")
+    q[0, 5, 9] = float("inf")
+    q[0, 6] *= 5
+    q = q.to(torch.bfloat16)
+    o, lse = fa.kv4_decode(q.cuda(), cache, _i32([128]))
+    assert fa.check() == 0
+    rows = [0, 1, 2, 3, 6, 7]
+    ref, tol, rl = P.decode(q[:, rows], kv, vv, vp, [128], 0, 0, 128 ** -0.5)
+    P.check(o[:, rows], ref, tol, "O")
+    P.check_lse(lse[:, rows], rl)
+    assert bool(torch.isnan(o[0, [4, 5]].float()).all()) and bool(torch.isnan(lse[0, [4, 5]]).all())
+
+
 def test_decode_many_sequences():
     """More sequences than a block plans at once."""
     B, Hkv, d, Tk = 1500, 1, 64, 64
