@@ -1236,21 +1236,6 @@ extern "C" int fa_kv4_read(void* k, void* v, const void* k_codes, const void* k_
 
 namespace fa {
 
-// Codes as [pairs][Tk][d/2] bytes with box {d/2, 32, 1}, in the swizzle of
-// their row width.
-static int kv4_tmap(CUtensorMap* m, const void* base, uint64_t pairs, uint64_t Tk, int d) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return FA_ERR_CUDA;
-  const cuuint64_t dims[3] = {(cuuint64_t)d / 2, Tk, pairs};
-  const cuuint64_t strides[2] = {(cuuint64_t)d / 2, Tk * (d / 2)};
-  const cuuint32_t box[3] = {(cuuint32_t)d / 2, 32, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
-}
-
 // Workspace pieces: prefix, then (maximum, sum), then O of every slot.
 struct Kv4Ws {
   size_t ml, o, bytes;
@@ -1303,11 +1288,8 @@ extern "C" int fa_kv4_decode(const void* q, const void* k_codes, const void* k_p
   if ((st = sm_count(&nsm))) return st;
   Kv4DecodeParams p;
   memset(&p, 0, sizeof(p));
-  if (Tk_max > 0) {
-    st = kv4_tmap(&p.tm_k, k_codes, (uint64_t)B * Hkv, Tk_max, d);
-    if (!st) st = kv4_tmap(&p.tm_v, v_codes, (uint64_t)B * Hkv, Tk_max, d);
-    if (st) return st;
-  }
+  p.k_codes = reinterpret_cast<const uint8_t*>(k_codes);
+  p.v_codes = reinterpret_cast<const uint8_t*>(v_codes);
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
   p.ws_prefix = reinterpret_cast<int*>(base);
   p.ws_ml = reinterpret_cast<float*>(base + w.ml);
@@ -1318,7 +1300,6 @@ extern "C" int fa_kv4_decode(const void* q, const void* k_codes, const void* k_p
   p.window = window;
   p.sinks = sinks;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.wait_limit_ns = kWaitLimitNs;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   for (int b0 = 0; b0 < B; b0 += kKv4MaxSeqs) {
     p.B = std::min(B - b0, kKv4MaxSeqs);

@@ -320,16 +320,17 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
 // whatever the lengths are.  A block's stretch of one (sequence, KV head) ends
 // in a partial result (slot: block + pair, both grow along the list), and a
 // second kernel joins them.  Each warp of a block takes 32 keys of every tile
-// through a ring of its own, which it fills itself: no warp waits for another
-// before a stretch ends, and none is spent on loading, so that 16 warps of 128
-// registers compute on an SM.
+// through a ring of its own, which all its lanes fill with 16-byte asynchronous
+// copies: no warp waits for another before a stretch ends, none is spent on loading,
+// and a slice costs ten copies (as four bulk copies issued by one lane it cost the
+// warp about twice the instructions, and 313 us where the copies take 297).
 static constexpr int kKv4MaxSeqs = 1024;  // sequences per launch
 static constexpr int kKv4MaxGrid = 1024;
 
 struct Kv4DecodeParams {
-  CUtensorMap tm_k;        // codes [B * Hkv][Tk_max][d/2] bytes, box {d/2, 32, 1}, swizzled
-  CUtensorMap tm_v;
   const __nv_bfloat16* q;  // [B][Hq][d]
+  const uint8_t* k_codes;  // [B][Hkv][Tk_max][d/2]
+  const uint8_t* v_codes;
   const __nv_bfloat16* k_params;  // [B][Hkv][Tk_max][2 d/32]
   const __nv_bfloat16* v_params;
   const int* seqlens;      // [B]
@@ -343,7 +344,6 @@ struct Kv4DecodeParams {
   int n_cta;
   int window, sinks;       // window > 0: only the last `window` keys and the first `sinks`
   float scale_log2;
-  unsigned long long wait_limit_ns;
 };
 
 // Visible tiles of a sequence: 0 .. n_sink - 1, then lo_tile ..; `count` in all.
@@ -374,18 +374,16 @@ struct Kv4Cfg {
   static constexpr int OFF_ML = OFF_MRG + NWARP * G * D * 2;     // m, l: [NWARP][8] each
   static constexpr int OFF_PRE = OFF_ML + 2 * NWARP * 8 * 4;     // prefix [kKv4MaxSeqs + 1]
   static constexpr int OFF_SCAN = OFF_PRE + (kKv4MaxSeqs + 4) * 4;
-  static constexpr int OFF_BAR = OFF_SCAN + 64;                  // full [NWARP][NSTAGE]
-  static constexpr int OFF_FLAG = OFF_BAR + NWARP * NSTAGE * 8;
-  static constexpr int SMEM_BYTES = OFF_FLAG + 16 + 1024;        // + alignment slack
-  static constexpr int CTAS = 4;                                 // per SM
+  static constexpr int SMEM_BYTES = OFF_SCAN + 64 + 1024;        // + alignment slack
+  // Blocks per SM: 12 warps of 168 registers at d = 128 (285 us on 64 sequences of
+  // 1k to 32k keys; 16 of 128 take 297), 16 of 128 at d = 64 (178; 12 take 186).
+  static constexpr int CTAS = D == 128 ? 3 : 4;
   static constexpr float RESCALE_THRESHOLD = 8.0f;
-  // the 64-byte swizzle repeats every 512 bytes, the 32-byte one every 256
-  static_assert(STAGE_BYTES % 512 == 0 && OFF_V % 512 == 0, "swizzled tiles need their alignment");
   static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "shared memory of an SM");
 };
 
-// Byte offset of 16-byte chunk c of row r of a code tile (the 64-byte swizzle
-// for 64-byte rows, the 32-byte one for 32-byte rows).
+// Byte offset of 16-byte chunk c of row r of a code tile: the chunk is moved so
+// that the 8 rows of an ldmatrix fall into different banks.
 template <int D>
 __device__ __forceinline__ uint32_t kv4_swz(int r, int c) {
   if constexpr (D == 128) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
@@ -433,6 +431,20 @@ __device__ __forceinline__ bool bf16x2_any_gt(uint32_t x, uint32_t lim) {
       : "=r"(r)
       : "r"(x), "r"(lim));
   return r != 0;
+}
+
+// Asynchronous copy of N bytes, global to shared, past L1 where N is 16.
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // The steps of one row's params, as words of two.
@@ -488,21 +500,9 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
   float* l_s = m_s + C::NWARP * 8;
   int* pre = reinterpret_cast<int*>(smem + C::OFF_PRE);
   int* scan = reinterpret_cast<int*>(smem + C::OFF_SCAN);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);
-  volatile int* stop_flag = abort_flag + 1;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // this warp's barriers and ring
-  auto bar_full = [&](int s) { return sbase + C::OFF_BAR + 8u * (warp * C::NSTAGE + s); };
-  const uint32_t ring_off = warp * C::NSTAGE * C::STAGE_BYTES;
-  WaitCtl wc{abort_flag, p.wait_limit_ns};
-
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
-    *stop_flag = 0;
-    for (int s = 0; s < C::NWARP * C::NSTAGE; ++s) mbar_init(sbase + C::OFF_BAR + 8u * s, 1);
-    fence_barrier_init();
-  }
+  const uint32_t ring_off = warp * C::NSTAGE * C::STAGE_BYTES;  // this warp's ring
   // ---- prefix sum of the sequences' visible tiles, the same in every block
   {
     constexpr int PER = kKv4MaxSeqs / C::THREADS + 1;  // up to and with the total at index B
@@ -541,9 +541,6 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
 
   const int g = lane >> 2, t4 = lane & 3;
   const Kv4PairsF16 codes16;
-  bool ok = true;
-  uint32_t phases = 0;  // bit s: parity of the next use of stage s
-
   // Lane offsets into a stage; rows 8 or 16 further on have the same swizzle,
   // and the second pair of V's chunks is the first with chunk bit 1 flipped.
   const uint32_t off_k = C::OFF_K + (D == 128 ? kv4_swz<D>(lane & 7, lane >> 3)
@@ -557,25 +554,32 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
   auto needed = [&](const Kv4Stretch& sg, int ks) {
     return ks < sg.len && (ks + C::SLICE > sg.lo || ks < p.sinks);
   };
+  // The warp copies its slice of tile j itself, 16 bytes a lane (8 for params at
+  // d = 64), as one asynchronous group; a slice that is not needed, or past the
+  // stretch, is an empty group, so that groups count tiles.
+  constexpr int ROWS = 512 / C::CB;  // rows of a warp-wide copy of codes
+  const uint32_t dst_c = sbase + ring_off + kv4_swz<D>(lane * 16 / C::CB, lane % (C::CB / 16));
+  const uint32_t dst_p = sbase + ring_off + C::OFF_KP + lane * C::PB;
   auto load = [&](const Kv4Stretch& sg, int j) {
     const int ks = key_of(sg, j);
-    if (lane == 0 && j < sg.n && needed(sg, ks)) {
-      const int s = j % C::NSTAGE;
-      const int pair = p.pair0 + sg.pair;
-      const uint32_t st = sbase + ring_off + s * C::STAGE_BYTES;
-      const size_t row = (size_t)pair * p.Tk_max + ks;
-      mbar_arrive_expect_tx(bar_full(s), C::STAGE_BYTES);
-      tma_load_3d(st + C::OFF_K, &p.tm_k, bar_full(s), 0, ks, pair);
-      bulk_load(st + C::OFF_KP, p.k_params + row * 2 * NG, C::SLICE * C::PB, bar_full(s));
-      tma_load_3d(st + C::OFF_V, &p.tm_v, bar_full(s), 0, ks, pair);
-      bulk_load(st + C::OFF_VP, p.v_params + row * 2 * NG, C::SLICE * C::PB, bar_full(s));
+    if (j < sg.n && needed(sg, ks)) {
+      const uint32_t so = (j % C::NSTAGE) * C::STAGE_BYTES;
+      // slices of 32 rows are counted in 32 bits (checked on the host)
+      const uint32_t slice = (uint32_t)(p.pair0 + sg.pair) * (uint32_t)(p.Tk_max / C::SLICE) + (uint32_t)(ks / C::SLICE);
+      const uint8_t* kc = p.k_codes + (size_t)slice * (C::SLICE * C::CB) + lane * 16;
+      const uint8_t* vc = p.v_codes + (size_t)slice * (C::SLICE * C::CB) + lane * 16;
+#pragma unroll
+      for (int i = 0; i < C::SLICE / ROWS; ++i) {
+        cp_async<16>(dst_c + so + C::OFF_K + 512 * i, kc + 512 * i);
+        cp_async<16>(dst_c + so + C::OFF_V + 512 * i, vc + 512 * i);
+      }
+      cp_async<C::PB>(dst_p + so, reinterpret_cast<const uint8_t*>(p.k_params) + (size_t)slice * (C::SLICE * C::PB) + lane * C::PB);
+      cp_async<C::PB>(dst_p + so + (C::OFF_VP - C::OFF_KP),
+                      reinterpret_cast<const uint8_t*>(p.v_params) + (size_t)slice * (C::SLICE * C::PB) + lane * C::PB);
     }
+    cp_async_commit();
   };
 
-  if (lane == 0) {
-    tma_prefetch_desc(&p.tm_k);
-    tma_prefetch_desc(&p.tm_v);
-  }
   Kv4Stretch sg(p, pre, at, left, C::TILE, warp * C::SLICE);
 #pragma unroll
   for (int j = 0; j < C::NSTAGE; ++j) load(sg, j);
@@ -674,9 +678,8 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
         load(sg, j + C::NSTAGE);
         continue;
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_full(s), (phases >> s) & 1u, wc));
-      if (!ok) break;
-      phases ^= 1u << s;
+      cp_async_wait<C::NSTAGE - 1>();  // all groups but those of the tiles after this one
+      __syncwarp();
       const bool whole = ks + C::SLICE <= sg.len && (ks >= sg.lo || ks + C::SLICE <= p.sinks);
       auto visible = [&](int key) { return key < sg.len && (key >= sg.lo || key < p.sinks); };
       if (!whole) {
@@ -688,7 +691,6 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
 #pragma unroll
           for (int i = 0; i < C::PB / 4; ++i) row[i] = 0u;
         }
-        fence_proxy_async_smem();  // before the next bulk load into this stage
         __syncwarp();
       }
       const uint32_t st = sbase + ring_off + s * C::STAGE_BYTES;
@@ -843,7 +845,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
 
     // the next stretch's first loads fly while this one's results are joined
     const size_t slot = (size_t)blockIdx.x + sg.pair;
-    if (left > 0 && ok) {
+    if (left > 0) {
       sg = Kv4Stretch(p, pre, at, left, C::TILE, warp * C::SLICE);
 #pragma unroll
       for (int j = 0; j < C::NSTAGE; ++j) load(sg, j);
@@ -887,17 +889,11 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
         p.ws_o[(slot * G + gg) * D + h * (D / 2) + dd] = O;
         if (h == 0 && dd == 0) *reinterpret_cast<float2*>(&p.ws_ml[(slot * G + gg) * 2]) = make_float2(M, L);
       }
-      // After an expired wait every warp still passes the same barriers; all
-      // stop together.
-      if (h == 1 && threadIdx.x == 0) *stop_flag = *abort_flag;
       __syncthreads();
     }
-    if (!more || *stop_flag) break;
+    if (!more) break;
   }
-  if (*stop_flag && lane == 0) {
-    // after an expired wait: every copy this warp issued lands before the block's memory goes
-    for (int s = 0; s < C::NSTAGE; ++s) mbar_wait_drain(bar_full(s), (phases >> s) & 1u, p.wait_limit_ns);
-  }
+  cp_async_wait<0>();
 }
 
 // One warp per (sequence, query head): the partial results of its stretch of
