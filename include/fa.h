@@ -421,8 +421,10 @@ int fa_decode_merge(const float* o_parts, size_t o_stride, const float* lse_part
  *               batch, token and head dims, in elements, each >= 0 and a multiple
  *               of 8.  An input may be a slice of a packed projection or
  *               broadcast; no two elements of an output may share their place.
- *               An output is its own input (same pointer, same strides) or its
- *               memory range is apart from it.
+ *               An output is its own input (same pointer, same strides) or apart
+ *               from it, and apart from the other tensor and its output: in
+ *               another range of memory, or another slice of the heads of the same
+ *               packed rows (the same batch and token strides).
  *   positions   DEVICE int32 [B,T], or NULL: row t has position t
  *   freqs       DEVICE fp64 [rotary_dim / 2], radians per position.  Angles are
  *               formed in 64 bits.
@@ -455,6 +457,8 @@ int fa_rope_backward(const void* dq, void* dq_out, const void* dk, void* dk_out,
  *   k_params, v_params  bf16 [B][Hkv][Tk_max][2 d/32]: the row's steps, then its
  *                       centres
  * Tk_max must be a multiple of 64, d 64 or 128.  Offsets are 64-bit.
+ * B == 0, T == 0 (append, read) and Tk_max == 0 are valid; T and Tk_max are at
+ * most 2^30, Hkv (append, read) at most 2^24.
  *
  * fa_kv4_append -- rows k, v bf16 [B,T,Hkv,d] (last dim contiguous; `strides` a
  * HOST array of 6: batch, token and head stride of k, then of v, in elements,
@@ -483,8 +487,10 @@ int fa_kv4_read(void* k, void* v, const void* k_codes, const void* k_params, con
  *           one, sinks > 0 is FA_ERR_INVALID_ARG);
  *   ws/ws_bytes  at least fa_kv4_decode_workspace_bytes(); contents on entry do
  *           not matter.
- * Hq/Hkv must be 1, 2, 4 or 8.  Rows that the query does not see may hold
- * anything.  The same inputs give the same bits.
+ * Hq/Hkv must be 1, 2, 4 or 8, and B * Hkv * Tk_max at most 2^36.  Rows that the
+ * query does not see may hold anything.  The same inputs give the same bits.
+ * q and p times V's step are multiplied as fp16 with a factor per row, which
+ * reaches |q| < 2^118 and steps below 2^107; past them a row comes out non-finite.
  */
 size_t fa_kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int Tk_max, int d);
 int fa_kv4_decode(const void* q, const void* k_codes, const void* k_params, const void* v_codes,

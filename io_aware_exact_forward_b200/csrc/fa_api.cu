@@ -1029,28 +1029,67 @@ static bool rope_dense_enough(const int64_t* st, int B, int T, int H, int d) {
   return true;
 }
 
-static int64_t rope_extent(const int64_t* st, int B, int T, int H, int d) {
-  return st[0] * (B - 1) + st[1] * (T - 1) + st[2] * (H - 1) + d;
+// Whether x (Hx heads) may share memory with y (Hy heads): no, if it can be
+// shown that their ranges are apart, or that they are different slices of the
+// same repeating slots (heads of the same packed rows or batches).
+static bool rope_collide(const void* x, const int64_t* sx, int Hx, const void* y, const int64_t* sy, int Hy, int B,
+                         int T, int d) {
+  const int64_t n[2] = {B, T};
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
+  const bool y_first = y0 < x0;
+  const int64_t diff = (int64_t)(y_first ? x0 - y0 : y0 - x0) / 2;
+  // Slots are counted over the axes in `outer` (bit 0: sequences, bit 1: tokens),
+  // which both must step through alike; the others belong to the slice.
+  for (int outer = 0; outer < 4; ++outer) {
+    int64_t ex = sx[2] * (Hx - 1) + d, ey = sy[2] * (Hy - 1) + d;  // a slice's extent
+    int64_t step[2] = {0, 0}, count[2] = {1, 1};
+    int axes = 0;
+    bool alike = true;
+    for (int a = 0; a < 2; ++a) {
+      if (n[a] == 1) continue;
+      if (outer >> a & 1) {
+        alike = alike && sx[a] == sy[a];
+        step[axes] = sx[a];
+        count[axes++] = n[a];
+      } else {
+        ex += sx[a] * (n[a] - 1);
+        ey += sy[a] * (n[a] - 1);
+      }
+    }
+    if (!alike) continue;
+    const int64_t front = y_first ? ey : ex, back = y_first ? ex : ey;  // in memory's order
+    if (axes == 0) {
+      if (diff >= front) return false;
+      continue;
+    }
+    const int in = axes == 2 && step[1] < step[0] ? 1 : 0;  // the inner of the stepping axes
+    const int64_t slot = step[in];
+    if (slot < 1) continue;  // broadcast: nothing to count by
+    const bool even = axes == 1 || step[1 - in] % slot == 0;          // slots repeat throughout
+    const bool nested = axes == 1 || step[1 - in] >= slot * count[in];  // slots never overlap
+    const int64_t off = even ? diff % slot : diff;
+    if ((even || nested) && off >= front && off + back <= slot) return false;
+  }
+  return true;
 }
 
 // Checks one tensor and its output (strides st[0..2] and st[3..5]).
 static int rope_tensor(RopeTensor* r, const void* x, void* y, const int64_t* st, const int64_t* so, int B, int T,
                        int H, int d) {
   if (!x || !y) return FA_ERR_INVALID_ARG;
+  const int64_t n[3] = {B, T, H};
+  bool same = x == y;  // in place: the same memory, the same strides
   for (int i = 0; i < 3; ++i) {
-    // 2^40 elements per step, so that offsets cannot leave 64 bits
-    if (st[i] < 0 || so[i] < 0 || st[i] > (1ll << 40) || so[i] > (1ll << 40)) return FA_ERR_INVALID_ARG;
+    // 2^60 elements per axis, so that offsets cannot leave 64 bits
+    const int64_t most = (1ll << 60) / n[i];
+    if (st[i] < 0 || so[i] < 0 || st[i] > most || so[i] > most) return FA_ERR_INVALID_ARG;
+    same = same && (n[i] == 1 || st[i] == so[i]);
   }
   if (!rope_dense_enough(so, B, T, H, d)) return FA_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(y)) return FA_ERR_ALIGNMENT;
   for (int i = 0; i < 3; ++i)
     if ((st[i] & 7) || (so[i] & 7)) return FA_ERR_ALIGNMENT;
-  // in place (the same memory, the same strides) or apart
-  const bool same = x == y && st[0] == so[0] && st[1] == so[1] && st[2] == so[2];
-  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
-  const uintptr_t x1 = x0 + 2 * (uintptr_t)rope_extent(st, B, T, H, d);
-  const uintptr_t y1 = y0 + 2 * (uintptr_t)rope_extent(so, B, T, H, d);
-  if (!same && x0 < y1 && y0 < x1) return FA_ERR_INVALID_ARG;
+  if (!same && rope_collide(x, st, H, y, so, H, B, T, d)) return FA_ERR_INVALID_ARG;
   r->x = reinterpret_cast<const __nv_bfloat16*>(x);
   r->y = reinterpret_cast<__nv_bfloat16*>(y);
   r->xb = st[0]; r->xt = st[1]; r->xh = st[2];
@@ -1076,6 +1115,12 @@ static int rope_impl(const void* q, void* q_out, const void* k, void* k_out, con
   if (Hq > 0) st = rope_tensor(&p.q, q, q_out, strides, strides + 3, B, T, Hq, d);
   if (!st && Hkv > 0) st = rope_tensor(&p.k, k, k_out, strides + 6, strides + 9, B, T, Hkv, d);
   if (st) return st;
+  // one tensor's output may not touch the other tensor
+  if (Hq > 0 && Hkv > 0 &&
+      (rope_collide(q_out, strides + 3, Hq, k_out, strides + 9, Hkv, B, T, d) ||
+       rope_collide(q_out, strides + 3, Hq, k, strides + 6, Hkv, B, T, d) ||
+       rope_collide(k_out, strides + 9, Hkv, q, strides, Hq, B, T, d)))
+    return FA_ERR_INVALID_ARG;
   p.positions = positions;
   p.freqs = freqs;
   p.n_tokens = (long long)B * T;
@@ -1143,7 +1188,7 @@ static int kv4_rows_blocks(Kv4RowsParams* p, int B, int T, int Hkv, int Tk_max, 
   p->Tk_max = Tk_max;
   // Eight steps along the tokens where that still leaves four blocks a
   // multiprocessor, fewer where it does not.
-  if (Hkv > (1 << 24)) return FA_ERR_INVALID_ARG;
+  if (Hkv > (1 << 24) || T > (1 << 30)) return FA_ERR_INVALID_ARG;
   p->heads = Hkv >= 2 ? 2 : 1;
   p->parts = (Hkv + p->heads - 1) / p->heads;
   p->tokens = 256 / (p->heads * (d / 8));

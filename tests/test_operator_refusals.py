@@ -76,7 +76,7 @@ def test_rope_arguments(mem):
     dense = (T * H * d, H * d, d)
     st = strides(*dense * 4)
 
-    def call(q=0, q_out=1024, k=2048, k_out=3072, st=st, freqs=4096, rot=64, inter=0, amp=1.0, B=1, T=T, Hq=H,
+    def call(q=0, q_out=1024, k=2048, k_out=3200, st=st, freqs=4096, rot=64, inter=0, amp=1.0, B=1, T=T, Hq=H,
              Hkv=H, d=d, pos=N):
         p = lambda x: N if x is None else mem(x)  # noqa: E731
         return lib.fa_rope(p(q), p(q_out), p(k), p(k_out), st, pos, p(freqs), rot, inter, amp, B, T, Hq, Hkv, d, N)
@@ -100,6 +100,28 @@ def test_rope_arguments(mem):
     assert call(st=strides(-8, H * d, d, *dense * 3)) == INVALID
     assert call(st=strides(*dense, 0, 0, d, *dense * 2)) == INVALID
     assert call(st=strides(*dense, T * H * d, d, d, *dense * 2)) == INVALID
+    # one output for both; q's output over k; k's output over q
+    assert call(k_out=1024) == INVALID and call(q_out=2048) == INVALID and call(k_out=128) == INVALID
+    # packed rows of 6 heads: q is heads 0, 1 and k heads 2, 3 of the same rows.  In
+    # place and into heads of another packed tensor the ranges interleave, which is
+    # no collision: the call gets as far as the device (there is none here)
+    row = 6 * d
+    packed = strides(*(T * row, row, d) * 4)
+    tokens_out = strides(*(row, 2 * row, d) * 4)  # [T, B, heads, d]
+    heads_out = strides(*(6 * T * d, d, T * d) * 4)  # [B, heads, T, d]
+    if not torch.cuda.is_available():
+        for st, k in ((packed, 2 * d * 2), (tokens_out, 2 * d * 2), (heads_out, 2 * T * d * 2)):
+            assert call(q=0, q_out=0, k=k, k_out=k, st=st, B=2) != INVALID
+            assert call(q=0, q_out=k // 2, k=k, k_out=k, st=st, B=2) == INVALID
+            # two heads further
+            assert call(q=0, q_out=2 * k, k=k, k_out=k, st=st, B=2) != INVALID
+    # heads 1, 2 for k overlap q's heads 0, 1
+    assert call(q=0, q_out=0, k=2 * d, k_out=2 * d, st=packed) == INVALID
+    # broadcast inputs step by nothing; steps that would leave 64 bits
+    assert call(q=0, q_out=0, k=256, k_out=1024, st=strides(*dense * 2, 0, 0, d, *dense), B=2) == INVALID
+    assert call(st=strides(*dense * 3, 1 << 60, H * d, d), B=2) == INVALID
+    # k's output one token further than k
+    assert call(q=0, q_out=0, k=2 * d * 2, k_out=2 * d * 2 + 2 * row, st=packed) == INVALID
     for f in (lib.fa_rope_backward,):
         assert f(N, N, N, N, st, N, mem(0), 64, 0, 1.0, 1, T, H, H, 96, N) == UNSUPPORTED
 
@@ -114,7 +136,7 @@ def test_kv4_arguments(mem):
 
     assert append(d=96) == UNSUPPORTED
     assert append(Tk=65) == INVALID and append(Tk=-64) == INVALID and append(T=-1) == INVALID
-    assert append(Hkv=0) == INVALID
+    assert append(Hkv=0) == INVALID and append(T=(1 << 30) + 1) == INVALID
     assert append(B=0) == 0 and append(T=0) == 0 and append(Tk=0) == 0
     assert append(k=None) == INVALID and append(codes=None) == INVALID and append(start=None) == INVALID
     assert append(k=8) == ALIGN and append(codes=1032) == ALIGN and append(start=2049) == ALIGN

@@ -248,3 +248,21 @@ def test_bad_calls():
         fa.kv4_append(x, x, cache, None)
     with pytest.raises(ValueError):
         fa.kv4_read(fa.KV4Cache(cache[0], cache[1][:, :, :32], cache[2], cache[3]), n, 1)
+
+
+def test_empty_calls():
+    """No sequences, no rows, no keys."""
+    c0 = fa.kv4_cache(0, 2, 64, 64)
+    o, lse = fa.kv4_decode(torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda"), c0, _i32([]))
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    c1 = fa.kv4_cache(2, 2, 0, 64)
+    o, lse = fa.kv4_decode(torch.ones(2, 4, 64, dtype=torch.bfloat16, device="cuda"), c1, _i32([0, 3]))
+    assert not o.any() and bool(torch.isneginf(lse).all())
+    c2 = fa.kv4_cache(2, 2, 64, 64)
+    x = torch.zeros(2, 0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    fa.kv4_append(x, x, c2, _i32([0, 0]))
+    k, v = fa.kv4_read(c2, _i32([0, 0]), 0)
+    assert k.shape == (2, 0, 2, 64)
+    k, v = fa.kv4_read(c1, _i32([0, 0]), 3)
+    assert not k.any() and not v.any()
+    assert fa.check() == 0

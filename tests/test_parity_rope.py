@@ -111,3 +111,18 @@ def test_rope_gradient_against_differences():
     ref = P.rope(g, freqs, pos, rot, amplitude=amp, inverse=True)
     bound = float((P.rope_tol(g, ref, rot, False, amp) * u.double().abs()).sum())
     assert abs(float((y.double().cpu() * u.double()).sum()) - diff) <= bound + 1e-9
+
+
+def test_rope_empty_and_graph():
+    f = fa.rope_frequencies(64)[0].cuda()
+    x = torch.zeros(2, 0, 3, 64, dtype=torch.bfloat16, device="cuda")
+    assert fa.rope(x, x, f)[0].shape == (2, 0, 3, 64)
+    q, pos = _rand((3, 1, 4, 64), 11).cuda(), torch.zeros(3, 1, dtype=torch.int32, device="cuda")
+    fa.rope(q, None, f, pos)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y, _ = fa.rope(q, None, f, pos)
+    pos.fill_(77)
+    g.replay()
+    assert torch.equal(y, fa.rope(q, None, f, pos)[0])
+    assert fa.check() == 0

@@ -177,3 +177,23 @@ def test_sink_decode_is_the_last_row_of_the_forward():
     P.check(o[:, -1:], ref, tol, "forward")
     P.check(od[:, None], ref, tol, "decode")
     assert float((lse[0, :, -1] - ld[0]).abs().max()) <= 2 * P.LSE_TOL
+
+
+@pytest.mark.parametrize("deterministic", [False, True])
+@pytest.mark.parametrize("B,Tq,Tk", [(0, 5, 5), (1, 0, 200), (1, 200, 0)])
+def test_sink_empty_calls(B, Tq, Tk, deterministic):
+    q, do = (torch.ones(B, Tq, 4, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, v = (torch.ones(B, Tk, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    o, lse = fa.forward(q, k, v, window=10, sinks=3)
+    assert not o.any() and bool(torch.isneginf(lse).all())
+    for x in fa.backward(q, k, v, o, lse, do, window=10, sinks=3, deterministic=deterministic):
+        assert not x.any()
+    assert fa.check() == 0
+
+
+def test_sink_decode_without_keys():
+    q = torch.ones(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    c = torch.full((2, 64, 2, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    o, lse = fa.decode_splitkv(q, c, c, torch.zeros(2, dtype=torch.int32, device="cuda"), window=5, sinks=2)
+    assert not o.any() and bool(torch.isneginf(lse).all())
+    assert fa.check() == 0
