@@ -92,9 +92,10 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // divided out once; a block has two heads of 8 tokens (d = 128; 16 at 64) side by
 // side, so that it meets 512 contiguous bytes on either side at a time.  They are bound by HBM (2 bytes an element on one side and
 // 0.625 on the other) and, closely behind, by issue: 32k tokens of 8 heads of 128
-// take the bytes 27 us each way.  One index per unit divided out in 64 bits and a
-// division per element took 110 and 56 us, in 32 bits without the divisions 64 and
-// 45.
+// take the bytes 27 us each way; append takes 54 us (165 instructions per warp and
+// unit, half of them on the half-rate integer pipe) and read 31.  One index per unit
+// divided out in 64 bits and a division per element took 110 and 56 us, in 32 bits
+// without the divisions 64 and 45.
 struct Kv4Place {
   int b, h, ch, t;  // sequence, head, unit of the row, first token
   bool in;
@@ -171,59 +172,59 @@ __global__ void __launch_bounds__(256) fa_kv4_append_kernel(const __grid_constan
   const long long xt = p.xt[which];
   constexpr int U = 4;  // loads in flight
   for (int n0 = 0; n0 < p.steps; n0 += U) {
-   uint4 raw[U];
+    uint4 raw[U];
 #pragma unroll
-   for (int u = 0; u < U; ++u) {
-     // every thread takes part in the shuffles; one past the end reads row 0
-     const int t = w.t + (n0 + u) * p.tokens;
-     raw[u] = *reinterpret_cast<const uint4*>(x + (w.in && n0 + u < p.steps && t < p.T ? t : 0) * xt);
-   }
-#pragma unroll
-   for (int u = 0; u < U; ++u) {
-    if (n0 + u >= p.steps) break;
-    const int t = w.t + (n0 + u) * p.tokens;
-    const uint32_t rw[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-    auto pair = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
-    auto bits = [](__nv_bfloat162 w) { return *reinterpret_cast<const uint32_t*>(&w); };
-    uint32_t lo2 = bits(__hmin2_nan(__hmin2_nan(pair(rw[0]), pair(rw[1])), __hmin2_nan(pair(rw[2]), pair(rw[3]))));
-    uint32_t hi2 = bits(__hmax2_nan(__hmax2_nan(pair(rw[0]), pair(rw[1])), __hmax2_nan(pair(rw[2]), pair(rw[3]))));
-#pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
-      lo2 = bits(__hmin2_nan(pair(lo2), pair(__shfl_xor_sync(0xffffffffu, lo2, off))));
-      hi2 = bits(__hmax2_nan(pair(hi2), pair(__shfl_xor_sync(0xffffffffu, hi2, off))));
+    for (int u = 0; u < U; ++u) {
+      // every thread takes part in the shuffles; one past the end reads row 0
+      const int t = w.t + (n0 + u) * p.tokens;
+      raw[u] = *reinterpret_cast<const uint4*>(x + (w.in && n0 + u < p.steps && t < p.T ? t : 0) * xt);
     }
-    const float lo = min_nan(bf16_lo(lo2), bf16_hi(lo2)), hi = max_nan(bf16_lo(hi2), bf16_hi(hi2));
-    const __nv_bfloat16 sb = __float2bfloat16_rn(div_7_5(__fsub_rn(0.5f * hi, 0.5f * lo)));
-    const float s = __bfloat162float(sb);
-    const __nv_bfloat16 zb = __float2bfloat16_rn(fmaf(8.f, s, lo));  // 8 s alone may overflow
-    const float z = __bfloat162float(zb);
-    float2 v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(make_float2(bf16_lo(rw[e]), bf16_hi(rw[e])), make_float2(-z, -z));
-    const uint32_t word = kv4_codes(v, s);
-    // the row's steps and centres at its first thread, for one store
-    const __nv_bfloat162 sz = __halves2bfloat162(sb, zb);
-    const uint32_t w0 = bits(sz);
-    const uint32_t w1 = __shfl_down_sync(0xffffffffu, w0, 4, CH);
-    uint32_t w2 = 0u, w3 = 0u;
-    if constexpr (NG == 4) {
-      w2 = __shfl_down_sync(0xffffffffu, w0, 8, CH);
-      w3 = __shfl_down_sync(0xffffffffu, w0, 12, CH);
-    }
-    const long long pos = (long long)start + t;
-    if (w.in && t < count && pos >= 0 && pos < p.Tk_max) {
-      *reinterpret_cast<uint32_t*>(codes + (size_t)pos * (D / 2)) = word;
-      if (w.ch == 0) {
-        const uint32_t s01 = __byte_perm(w0, w1, 0x5410), z01 = __byte_perm(w0, w1, 0x7632);
-        __nv_bfloat16* pr = params + (size_t)pos * (2 * NG);
-        if constexpr (NG == 4)
-          *reinterpret_cast<uint4*>(pr) = make_uint4(s01, __byte_perm(w2, w3, 0x5410), z01,
-                                                     __byte_perm(w2, w3, 0x7632));
-        else
-          *reinterpret_cast<uint2*>(pr) = make_uint2(s01, z01);
+    for (int u = 0; u < U; ++u) {
+      if (n0 + u >= p.steps) break;
+      const int t = w.t + (n0 + u) * p.tokens;
+      const uint32_t rw[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      auto pair = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+      auto bits = [](__nv_bfloat162 w) { return *reinterpret_cast<const uint32_t*>(&w); };
+      uint32_t lo2 = bits(__hmin2_nan(__hmin2_nan(pair(rw[0]), pair(rw[1])), __hmin2_nan(pair(rw[2]), pair(rw[3]))));
+      uint32_t hi2 = bits(__hmax2_nan(__hmax2_nan(pair(rw[0]), pair(rw[1])), __hmax2_nan(pair(rw[2]), pair(rw[3]))));
+#pragma unroll
+      for (int off = 1; off < 4; off <<= 1) {
+        lo2 = bits(__hmin2_nan(pair(lo2), pair(__shfl_xor_sync(0xffffffffu, lo2, off))));
+        hi2 = bits(__hmax2_nan(pair(hi2), pair(__shfl_xor_sync(0xffffffffu, hi2, off))));
+      }
+      const float lo = min_nan(bf16_lo(lo2), bf16_hi(lo2)), hi = max_nan(bf16_lo(hi2), bf16_hi(hi2));
+      const __nv_bfloat16 sb = __float2bfloat16_rn(div_7_5(__fsub_rn(0.5f * hi, 0.5f * lo)));
+      const float s = __bfloat162float(sb);
+      const __nv_bfloat16 zb = __float2bfloat16_rn(fmaf(8.f, s, lo));  // 8 s alone may overflow
+      const float z = __bfloat162float(zb);
+      float2 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __fadd2_rn(make_float2(bf16_lo(rw[e]), bf16_hi(rw[e])), make_float2(-z, -z));
+      const uint32_t word = kv4_codes(v, s);
+      // the row's steps and centres at its first thread, for one store
+      const __nv_bfloat162 sz = __halves2bfloat162(sb, zb);
+      const uint32_t w0 = bits(sz);
+      const uint32_t w1 = __shfl_down_sync(0xffffffffu, w0, 4, CH);
+      uint32_t w2 = 0u, w3 = 0u;
+      if constexpr (NG == 4) {
+        w2 = __shfl_down_sync(0xffffffffu, w0, 8, CH);
+        w3 = __shfl_down_sync(0xffffffffu, w0, 12, CH);
+      }
+      const long long pos = (long long)start + t;
+      if (w.in && t < count && pos >= 0 && pos < p.Tk_max) {
+        *reinterpret_cast<uint32_t*>(codes + (size_t)pos * (D / 2)) = word;
+        if (w.ch == 0) {
+          const uint32_t s01 = __byte_perm(w0, w1, 0x5410), z01 = __byte_perm(w0, w1, 0x7632);
+          __nv_bfloat16* pr = params + (size_t)pos * (2 * NG);
+          if constexpr (NG == 4)
+            *reinterpret_cast<uint4*>(pr) = make_uint4(s01, __byte_perm(w2, w3, 0x5410), z01,
+                                                       __byte_perm(w2, w3, 0x7632));
+          else
+            *reinterpret_cast<uint2*>(pr) = make_uint2(s01, z01);
+        }
       }
     }
-   }
   }
 }
 
@@ -319,11 +320,14 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
 // of (sequence, KV head), are one long list that the blocks share out evenly
 // whatever the lengths are.  A block's stretch of one (sequence, KV head) ends
 // in a partial result (slot: block + pair, both grow along the list), and a
-// second kernel joins them.  Each warp of a block takes 32 keys of every tile
-// through a ring of its own, which all its lanes fill with 16-byte asynchronous
-// copies: no warp waits for another before a stretch ends, none is spent on loading,
-// and a slice costs ten copies (as four bulk copies issued by one lane it cost the
-// warp about twice the instructions, and 313 us where the copies take 297).
+// second kernel joins them.  64 sequences of 1k to 32k keys (8 KV heads of 128,
+// 1.39 GB) take 285 us, 4.85 TB/s; the bytes alone would take 214.  What bounds it
+// then is issue: about 330 instructions per warp and 16 keys, at 0.6 a cycle.
+// Each warp of a block takes 32 keys of every tile through a ring of its own, which
+// all its lanes fill with 16-byte asynchronous copies: no warp waits for another
+// before a stretch ends, none is spent on loading, and a slice costs ten copies (as
+// four bulk copies issued by one lane it cost the warp about twice the
+// instructions, and 313 us where the copies take 297).
 static constexpr int kKv4MaxSeqs = 1024;  // sequences per launch
 static constexpr int kKv4MaxGrid = 1024;
 

@@ -13,7 +13,10 @@
 // turn goes to sincospif.  The angles of a token are shared by all its heads:
 // a block forms them once, in shared memory.
 //
-// Bound by HBM: 4 bytes per element and a few operations.
+// Bound by HBM: 4 bytes per element and a few operations.  32k tokens of 40 heads
+// of 128 out of a packed projection take 117 us, 5.7 TB/s; 64k tokens of 32 heads
+// of 64, half of each turned, 82 us, 6.5 TB/s.  A single step's 64 tokens take 5
+// us, the latency of a launch, the angles and one round trip to memory.
 #pragma once
 
 #include "fa_ptx.cuh"
