@@ -729,7 +729,7 @@ size_t fa_decode_workspace_bytes(int B, int Hq, int Tk_max, int d, int chunk) {
 // that a window can touch.
 static size_t decode_visible_chunks(int Tk_max, int chunk, int window, int sinks) {
   return std::min(decode_nchunk(Tk_max, chunk),
-                  (size_t)(sinks + chunk - 1) / chunk + ((size_t)window + chunk - 2) / chunk + 1);
+                  ((size_t)sinks + chunk - 1) / chunk + ((size_t)window + chunk - 2) / chunk + 1);
 }
 
 size_t fa_decode_sinks_workspace_bytes(int B, int Hq, int Tk_max, int d, int chunk, int window, int sinks) {
