@@ -408,7 +408,7 @@ def _decode_sinks(q, k_cache, v_cache, seqlens, scale, chunk, workspace, out, ls
     else:
         _demand("out", out, torch.bfloat16, index, (B, Hq, d))
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, Hq), dtype=torch.float32)
     else:
         _demand("lse", lse, torch.float32, index, (B, Hq))
     with _on_device(index):

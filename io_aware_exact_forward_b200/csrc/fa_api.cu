@@ -189,6 +189,23 @@ static int launch_status() {
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// Launches a kernel that calls pdl_wait() behind one that calls pdl_launch().
+template <typename P>
+static int launch_after(void (*kernel)(P), unsigned blocks, unsigned threads, cudaStream_t s, const P& p) {
+  cudaLaunchAttribute attr;
+  memset(&attr, 0, sizeof(attr));
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 // Checks shared by the prefill entry points.
 static int check_prefill(int B, int Hq, int Hkv, int Tq, int Tk, int d, float scale, int causal) {
   if (B < 0 || Hq < 1 || Hkv < 1 || Tq < 0 || Tk < 0) return FA_ERR_INVALID_ARG;
@@ -812,11 +829,8 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache, 
   const int warps = B * Hq;
   const int blocks = (warps * 32 + 255) / 256;
   if (sinks > 0) {
-    if (d == 64)
-      fa_decode_combine_kernel<64, true><<<blocks, 256, 0, s>>>(p);
-    else
-      fa_decode_combine_kernel<128, true><<<blocks, 256, 0, s>>>(p);
-    return launch_status();
+    return launch_after(d == 64 ? fa_decode_combine_kernel<64, true> : fa_decode_combine_kernel<128, true>, blocks, 256,
+                        s, p);
   }
   if (Tk_max > 0) {
     if (d == 64)
@@ -1368,11 +1382,8 @@ extern "C" int fa_kv4_decode(const void* q, const void* k_codes, const void* k_p
 #undef FA_KV4_LAUNCH
     if (st) return st;
     const unsigned blocks = (unsigned)(((size_t)p.B * Hq * 32 + 127) / 128);
-    if (d == 64)
-      fa_kv4_combine_kernel<64><<<blocks, 128, 0, s>>>(p);
-    else
-      fa_kv4_combine_kernel<128><<<blocks, 128, 0, s>>>(p);
-    if ((st = launch_status())) return st;
+    if ((st = launch_after(d == 64 ? fa_kv4_combine_kernel<64> : fa_kv4_combine_kernel<128>, blocks, 128, s, p)))
+      return st;
   }
   return FA_OK;
 }

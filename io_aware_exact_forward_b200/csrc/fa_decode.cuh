@@ -142,6 +142,7 @@ template <int D, int G, bool SINK = false>
 __global__ void __launch_bounds__(DecCfg<D, G>::THREADS)
 fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
   using C = DecCfg<D, G>;
+  if constexpr (SINK) pdl_launch();  // fa_decode_combine_kernel
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -437,6 +438,7 @@ __global__ void __launch_bounds__(256) fa_decode_combine_kernel(const __grid_con
   const int gw = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (gw >= p.B * p.Hq) return;
+  if constexpr (SINK) pdl_wait();
   const int b = gw / p.Hq;
   const int seqlen = clamp_seqlen(p, p.seqlens[b]);
   constexpr int E = D / 32;

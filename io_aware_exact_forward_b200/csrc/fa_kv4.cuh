@@ -507,6 +507,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t ring_off = warp * C::NSTAGE * C::STAGE_BYTES;  // this warp's ring
+  pdl_launch();  // fa_kv4_combine_kernel; its blocks need no shared memory and wait at their start
   // ---- prefix sum of the sequences' visible tiles, the same in every block
   {
     constexpr int PER = kKv4MaxSeqs / C::THREADS + 1;  // up to and with the total at index B
@@ -907,6 +908,7 @@ __global__ void __launch_bounds__(128) fa_kv4_combine_kernel(const __grid_consta
   constexpr int E = D / 32, U = 8;
   const int row = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   if (row >= p.B * p.Hq) return;
+  pdl_wait();
   const int G = p.Hq / p.Hkv;
   const int b = row / p.Hq, hkv = row % p.Hq / G, gq = row % G;
   const int before = p.ws_prefix[b], count = p.ws_prefix[b + 1] - before;

@@ -472,6 +472,13 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Programmatic dependent launch: the second of two kernels that belong together
+// is set up while the first still runs, and waits for its end, memory included,
+// in pdl_wait().  pdl_launch() in the first lets the second's blocks be placed
+// once every block of the first has passed it.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Bits 0 .. n - 1 (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t bits_below(int n) {
   uint32_t r;  // shl by 32 gives 0

@@ -122,7 +122,7 @@ def kv4_read(cache, start, T, count=None, out_k=None, out_v=None):
     else:
         _demand("out_k", out_k, torch.bfloat16, index, shape)
     if out_v is None:
-        out_v = kp.new_empty(shape)
+        out_v = torch.empty_like(out_k)
     else:
         _demand("out_v", out_v, torch.bfloat16, index, shape)
     with _on_device(index):
@@ -165,7 +165,7 @@ def kv4_decode(q, cache, seqlens, scale=None, window=None, sinks=0, workspace=No
     else:
         _demand("out", out, torch.bfloat16, index, (B, Hq, d))
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, Hq), dtype=torch.float32)
     else:
         _demand("lse", lse, torch.float32, index, (B, Hq))
     kc, kp, vc, vp = cache
