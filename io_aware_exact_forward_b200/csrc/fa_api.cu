@@ -805,6 +805,8 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache, 
   p.n_items = (int)((size_t)B * Hkv * n);
   p.window = window;
   p.sinks = sinks;
+  p.sink_chunks = (sinks + chunk - 1) / chunk;
+  p.inv_chunk = ((1ull << 40) + chunk / 64 - 1) / (chunk / 64);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = kWaitLimitNs;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -46,6 +46,8 @@ struct DecodeParams {
   int n_items;               // B * Hkv * nchunk (items past a sequence's end are skipped)
   int window;                // > 0: the query sees only the last `window` keys of its sequence
   int sinks;                 // SINK instantiation: and its first `sinks` keys
+  int sink_chunks;           // SINK: ceil(sinks / chunk)
+  unsigned long long inv_chunk;  // SINK: ceil(2^40 / (chunk / 64))
   float scale_log2;
   unsigned long long wait_limit_ns;
 };
@@ -106,14 +108,21 @@ __device__ __forceinline__ uint32_t swz_off(int key, int ch) {
 // split kernel wrote.
 __device__ __forceinline__ int clamp_seqlen(const DecodeParams& p, int n) { return min(max(n, 0), p.Tk_max); }
 
+// x / chunk for 0 <= x < 2^31: chunk is 64 m with m <= 64, and n = x / 64 < 2^25
+// makes n * ceil(2^40 / m) exceed n * 2^40 / m by less than 2^40 / m.
+__device__ __forceinline__ int div_chunk(const DecodeParams& p, int x) {
+  return (int)((unsigned long long)(x >> 6) * p.inv_chunk >> 40);
+}
+
 // Chunks of a sequence that hold a visible key when sinks stay visible behind
-// the window: chunks 0 .. n_sink - 1, then lo .. end - 1, `count` in all.
+// the window: chunks 0 .. n_sink - 1, then lo .. end - 1, `count` in all.  Worked
+// out for every item, skipped ones too: two divisions each showed.
 struct SinkChunks {
   int n_sink, lo, count;
   __device__ __forceinline__ SinkChunks(const DecodeParams& p, int seqlen) {
-    const int end = (seqlen + p.chunk - 1) / p.chunk;
-    n_sink = min(end, (p.sinks + p.chunk - 1) / p.chunk);
-    lo = max(n_sink, max(0, seqlen - p.window) / p.chunk);
+    const int end = div_chunk(p, seqlen + p.chunk - 1);
+    n_sink = min(end, p.sink_chunks);
+    lo = max(n_sink, div_chunk(p, max(0, seqlen - p.window)));
     count = n_sink + max(0, end - lo);
   }
   __device__ __forceinline__ int at(int v) const { return v < n_sink ? v : lo + v - n_sink; }
@@ -307,10 +316,19 @@ fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
       const int kb0 = i * C::SUB + kw + 2 * t4;
       float sc[4] = {s0[0], s0[1], s1[0], s1[1]};
       const int kk[4] = {kb0, kb0 + 1, kb0 + 8, kb0 + 9};
+      const int r0 = i * C::SUB + kw;
+      // SINK: the query sees all 16 keys (masking every tile element by element took
+      // 125 us where this takes 113: 64 sequences, W = 2048, 8 KV heads of 128)
+      const bool whole = SINK && r0 + 16 <= nkeys && (r0 >= klo || r0 + 16 <= nsk);
+      if (whole) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        sc[e] = (kk[e] < nkeys && (kk[e] >= klo || (SINK && kk[e] < nsk)) && real_row) ? sc[e] * p.scale_log2
-                                                                                     : -INFINITY;
+        for (int e = 0; e < 4; ++e) sc[e] = real_row ? sc[e] * p.scale_log2 : -INFINITY;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sc[e] = (kk[e] < nkeys && (kk[e] >= klo || (SINK && kk[e] < nsk)) && real_row) ? sc[e] * p.scale_log2
+                                                                                       : -INFINITY;
+      }
       float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -349,8 +367,7 @@ fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
         if constexpr (SINK) {
           // A masked key's P is 0, but 0 times what an unwritten cache row
           // may hold (NaN, infinity) is not: such rows are zeroed first.
-          const int r0 = i * C::SUB + kw;
-          if (r0 + 16 > nkeys || (r0 < klo && r0 + 16 > nsk)) {
+          if (!whole) {
             for (int idx = lane; idx < 16 * (D / 8); idx += 32) {
               const int r = idx / (D / 8);
               if (r0 + r >= nkeys || (r0 + r < klo && r0 + r >= nsk))
