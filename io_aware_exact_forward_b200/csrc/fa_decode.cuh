@@ -145,8 +145,24 @@ __device__ __forceinline__ int chunk_tile0(const DecodeParams& p, int k0, int se
   return max(0, seqlen - p.window - k0) / 64;
 }
 
-// Item k covers chunk k % nchunk of (sequence, KV head) k / nchunk; with SINK
-// the (k % nchunk)-th visible chunk, nchunk being the most that a sequence has.
+// Item k covers chunk k % nchunk of (sequence, KV head) k / nchunk.  With SINK c
+// counts visible chunks, nchunk being the most that a sequence has, and the KV
+// heads of a chunk, whose rows lie side by side, are adjacent in item order.
+template <bool SINK>
+__device__ __forceinline__ void item_place(const DecodeParams& p, int item, int& c, int& b, int& hkv) {
+  const int n = SINK ? p.Hkv : p.nchunk;
+  const int rest = item / n, low = item - rest * n;
+  if (SINK) {
+    hkv = low;
+    b = rest / p.nchunk;
+    c = rest - b * p.nchunk;
+  } else {
+    c = low;
+    b = rest / p.Hkv;
+    hkv = rest - b * p.Hkv;
+  }
+}
+
 template <int D, int G, bool SINK = false>
 __global__ void __launch_bounds__(DecCfg<D, G>::THREADS)
 fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
@@ -195,9 +211,8 @@ fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
       bool ok = true;
       int t = 0, qi = 0;  // ring slot counter and item counter, continuous across items
       for (int item = blockIdx.x; item < p.n_items && ok; item += gridDim.x) {
-        int c = item % p.nchunk;
-        const int bh = item / p.nchunk;
-        const int b = bh / p.Hkv, hkv = bh % p.Hkv;
+        int c, b, hkv;
+        item_place<SINK>(p, item, c, b, hkv);
         const int seqlen = seqlen_of(b);
         if constexpr (SINK) {
           const SinkChunks sc(p, seqlen);
@@ -247,10 +262,9 @@ fa_decode_split_kernel(const __grid_constant__ DecodeParams p) {
   bool ok = true;
   int t = 0, qi = 0;
   for (int item = blockIdx.x; item < p.n_items; item += gridDim.x) {
-    const int v_idx = item % p.nchunk;  // slot of this chunk's partial result
-    int c = v_idx;
-    const int bh = item / p.nchunk;
-    const int b = bh / p.Hkv, hkv = bh % p.Hkv;
+    int c, b, hkv;
+    item_place<SINK>(p, item, c, b, hkv);
+    const int v_idx = c;  // slot of this chunk's partial result
     const int seqlen = seqlen_of(b);
     if constexpr (SINK) {
       const SinkChunks sc(p, seqlen);
