@@ -266,3 +266,47 @@ def test_empty_calls():
     k, v = fa.kv4_read(c1, _i32([0, 0]), 3)
     assert not k.any() and not v.any()
     assert fa.check() == 0
+
+
+def test_append_and_read_in_a_graph():
+    B, T, Hkv, d, Tk = 2, 3, 2, 128, 128
+    x = _rand((B, T, Hkv, d), 83).cuda()
+    start, count = _i32([5, 60]), _i32([3, 2])
+    cache = fa.kv4_cache(B, Hkv, Tk, d)
+    fa.kv4_append(x, x, cache, start, count)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fa.kv4_append(x, x, cache, start, count)
+        k, v = fa.kv4_read(cache, start, T, count)
+    for b in range(2):  # the second replay appends behind the first's rows
+        x.copy_(_rand((B, T, Hkv, d), 84 + b))
+        g.replay()
+        values, _ = P.values4(*(t.cuda() for t in P.pack4(x.cpu().transpose(1, 2).contiguous())))
+        want = values.transpose(1, 2).to(torch.bfloat16)
+        want[1, 2] = 0
+        assert torch.equal(k.cpu(), want.cpu()) and torch.equal(v.cpu(), want.cpu())
+        start += 3
+    assert fa.check() == 0
+
+
+def test_offsets_past_32_bits():
+    """The last sequence of a cache whose codes alone pass 2^31 bytes, with all
+    rows but its last ones unwritten."""
+    B, Hkv, Tk, d, n = 66, 8, 65536, 128, 300
+    cache = fa.kv4_cache(B, Hkv, Tk, d)
+    assert cache.k_codes.numel() > 1 << 31
+    k, v = _rand((B, n, Hkv, d), 86), _rand((B, n, Hkv, d), 87)
+    count = [0] * (B - 1) + [n]
+    fa.kv4_append(k.cuda(), v.cuda(), cache, _i32([Tk - n] * B), _i32(count))
+    want = [P.values4(*(t.cuda() for t in P.pack4(x[-1:].transpose(1, 2).contiguous()))) for x in (k, v)]
+    rk, rv = fa.kv4_read(cache, _i32([Tk - n] * B), n, _i32(count))
+    for x, (y, _) in zip((rk, rv), want):
+        assert torch.equal(x[-1:].cpu(), y.transpose(1, 2).to(torch.bfloat16).cpu())
+    q = _rand((B, 16, d), 88)
+    o, lse = fa.kv4_decode(q.cuda(), cache, _i32([0] * (B - 1) + [Tk]), window=n)
+    assert fa.check() == 0
+    assert not o[:-1].any() and bool(torch.isneginf(lse[:-1]).all())
+    (kv, _), (vv, vp) = want
+    ref, tol, rl = P.decode(q[-1:], kv, vv, vp, [n], 0, 0, d ** -0.5)
+    P.check(o[-1:], ref, tol, "O")
+    P.check_lse(lse[-1:], rl)

@@ -126,3 +126,16 @@ def test_rope_empty_and_graph():
     g.replay()
     assert torch.equal(y, fa.rope(q, None, f, pos)[0])
     assert fa.check() == 0
+
+
+def test_rope_strides_past_32_bits():
+    T, step = 200, 1 << 24
+    big = torch.empty(T * step, dtype=torch.bfloat16, device="cuda")
+    x = big.as_strided((1, T, 3, 64), (T * step, step, 64, 1))
+    x.copy_(_rand((1, T, 3, 64), 12))
+    f = fa.rope_frequencies(64)[0].cuda()
+    want, _ = fa.rope(x.contiguous(), None, f)
+    got, _ = fa.rope(x, None, f)
+    assert torch.equal(got, want)
+    fa.rope(x, None, f, out_q=x)
+    assert torch.equal(x, want) and fa.check() == 0

@@ -197,3 +197,80 @@ def test_sink_decode_without_keys():
     o, lse = fa.decode_splitkv(q, c, c, torch.zeros(2, dtype=torch.int32, device="cuda"), window=5, sinks=2)
     assert not o.any() and bool(torch.isneginf(lse).all())
     assert fa.check() == 0
+
+
+def test_sink_decode_many_sequences():
+    """More sequences than a block keeps the lengths of."""
+    B, T, W, S = 1300, 64, 20, 3
+    q, k, v = _rand((B, 2, 64), 61), _rand((B, T, 1, 64), 62), _rand((B, T, 1, 64), 63)
+    lens = [i * 7 % 65 for i in range(B)]
+    o, lse = fa.decode_splitkv(q.cuda(), k.cuda(), v.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), chunk=64,
+                               window=W, sinks=S)
+    assert fa.check() == 0
+    ref, tol, rl = P.decode(q, k.double().transpose(1, 2), v.double().transpose(1, 2), None, lens, W, S, 64 ** -0.5)
+    P.check(o, ref, tol, "O")
+    P.check_lse(lse, rl)
+
+
+def test_sink_decode_streams_and_graphs():
+    """Two graphs with one workspace, replayed in turn after their inputs changed,
+    and two calls at once on streams of their own."""
+    B, T, W, S = 4, 1000, 300, 5
+    k, v = _rand((B, T, 2, 128), 64).cuda(), _rand((B, T, 2, 128), 65).cuda()
+    qs = [_rand((B, 8, 128), 66 + i).cuda() for i in range(2)]
+    lens = torch.tensor([1000, 3, 305, 0], dtype=torch.int32, device="cuda")
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+
+    def call(q, **kw):
+        return fa.decode_splitkv(q, k, v, lens, window=W, sinks=S, **kw)
+
+    want = [call(q) for q in qs]
+    streams, got = [torch.cuda.Stream() for _ in qs], []
+    for s, q in zip(streams, qs):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            got.append(call(q))
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for a, b in zip(got, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    graphs, outs = [], []
+    for q in qs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(q, workspace=ws))
+        graphs.append(g)
+    lens.copy_(torch.tensor([17, 1000, 0, 640], dtype=torch.int32))
+    k.copy_(k.flip(0))
+    for _ in range(2):
+        for g in graphs:
+            g.replay()
+    want = [call(q) for q in qs]
+    assert fa.check() == 0
+    for a, b in zip(outs, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_sink_training_step_in_a_graph(d):
+    T, W, S = 900, 130, 4
+    q, do = (_rand((1, T, 4, d), 70 + i).cuda() for i in range(2))
+    k, v = (_rand((1, T, 2, d), 72 + i).cuda() for i in range(2))
+    ws = torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
+
+    def step(**kw):
+        o, lse = fa.forward(q, k, v, window=W, sinks=S)
+        return (o, lse, *fa.backward(q, k, v, o, lse, do, window=W, sinks=S, deterministic=True, **kw))
+
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(workspace=ws)
+    for t in (q, k, v, do):
+        t.copy_(t.flip(1))
+    ws.fill_(255)
+    g.replay()
+    want = step()
+    assert fa.check() == 0
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
