@@ -300,13 +300,18 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
 // products of their own: z against sum q (in three bf16 parts, 24 bits), and p
 // against z.
 //
-// p s is formed in 32 bits and rounded to fp16 once (2^-12 of itself); l sums the
-// unrounded p.  fp16's range: p carries a power of two that brings the largest
-// step so far to 2^3 .. 2^4, lowered when a step eight times as large comes (then
-// the sums so far are rescaled, as for a moved maximum).  A p s that is 2^18 below
-// that loses bits and one 2^28 below it is dropped: that is p itself, or a key
-// whose steps are that much smaller than others that the same warp has met.  Steps
-// below 2^-70 or from 2^107 on leave fp16's range altogether.
+// p s is formed in 32 bits and rounded to fp16 once (2^-11 of itself); l sums the
+// unrounded p.  fp16's range: V's steps, and nothing else, carry a power of two
+// that brings the largest so far to 2^19 .. 2^20 against a p of 2^-16 and less (the
+// reference of the exponentials is 16 above the maximum, so that sums of p times
+// large centres have room).  It is lowered when a step eight times as large comes,
+// and the sums of the codes' part with it; m, l and the centres' part, and so the
+// log-sum-exp, do not depend on it. A p s that is 2^18
+// below the largest possible loses bits and one 2^28 below it is dropped: that is p
+// itself, or a key whose steps are that much smaller than others that the same warp
+// has met.  A slice's steps are scaled where they lie in shared
+// memory, a key by each lane (four instructions a slice; as factors on the
+// probabilities they would be sixteen).
 //
 // Operand layouts.  A 16-byte chunk of a row's codes is one group.  For K,
 // ldmatrix gives lane (g, t) of a warp the word of key g's dims 8t .. 8t + 7 of
@@ -330,6 +335,17 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
 // instructions, and 313 us where the copies take 297).
 static constexpr int kKv4MaxSeqs = 1024;  // sequences per launch
 static constexpr int kKv4MaxGrid = 1024;
+
+static constexpr int kKv4RefAbove = 16;  // exponentials' reference above the maximum, in log2 units
+
+// The powers of two on V's steps, of two groups in a bf16 pair: 2^126 at first
+// and at most, 2^-105 at least (any finite step is below 2^20 then).
+static constexpr uint32_t kKv4FactorMax = 0x7E807E80u;
+static constexpr uint32_t kKv4ScaledMax = 0x4B004B00u;  // 2^23: a step that is larger when scaled lowers its factor
+// The factor (its bf16 exponent) that brings a step, a bf16, to 2^19 .. 2^20.
+__device__ __forceinline__ int kv4_factor_exp(uint32_t step) {
+  return 277 - min(max((int)((step >> 7) & 0xFFu) + 4, 24), 255);
+}
 
 struct Kv4DecodeParams {
   const __nv_bfloat16* q;  // [B][Hq][d]
@@ -399,6 +415,12 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr));
   return r;
 }
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 r;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
@@ -427,6 +449,16 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t x, uint32_t y) {  // a number, of a number and a NaN
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
 }
 // Whether either of a bf16 pair is above its limit (NaN is not).
 __device__ __forceinline__ bool bf16x2_any_gt(uint32_t x, uint32_t lim) {
@@ -662,11 +694,9 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
     }
 
     float m_run = -INFINITY, l_part = 0.f;   // row g
-    // p carries a factor 2^lv that places p s in fp16's range: the steps seen so
-    // far are at most 2^(7 - lv), and p s at most 2^15.  `step_limit` is that bound
-    // as a bf16 pair.
-    float lv = 0.f;
-    uint32_t step_limit = 0u;
+    uint32_t fac[NG / 2];                    // what V's steps are scaled by, a pair of groups each
+#pragma unroll
+    for (int w = 0; w < NG / 2; ++w) fac[w] = kKv4FactorMax;
     float oacc[NG][2][4];                    // dims 32c + 4g + 2kk (+1), queries 2t, 2t + 1
     float zacc[4] = {0.f, 0.f, 0.f, 0.f};    // sum of p z, by group
 #pragma unroll
@@ -756,39 +786,53 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
       mx = fmax3(mx, sc[1][1].x, sc[1][1].y);
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const bool move = mx > m_run + C::RESCALE_THRESHOLD || (m_run == -INFINITY && mx != -INFINITY);
-      uint32_t sw[NG / 2];  // the steps of key `lane`
-      kv4_steps<NG>(st + C::OFF_VP + lane * C::PB, sw);
-      bool wide = bf16x2_any_gt(sw[0], step_limit);
-      if constexpr (NG == 4) wide |= bf16x2_any_gt(sw[1], step_limit);
-      if (__any_sync(0xffffffffu, move || wide)) {
-        float smax = fmaxf(bf16_lo(sw[0]), bf16_hi(sw[0]));
-        if constexpr (NG == 4) smax = fmaxf(smax, fmaxf(bf16_lo(sw[1]), bf16_hi(sw[1])));
+      const bool move = mx > m_run + (C::RESCALE_THRESHOLD - kKv4RefAbove) || (m_run == -INFINITY && mx != -INFINITY);
+      uint32_t ps[NG / 2];  // V's steps of key `lane`, scaled
+      const uint32_t at_sw = dst_p + s * C::STAGE_BYTES + (C::OFF_VP - C::OFF_KP);
+      kv4_steps<NG>(at_sw, ps);
+      bool wide = false;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, off));
-        // 2^lv brings the largest step into [2^3, 2^4), which leaves room for steps
-        // eight times as large
-        const float fit = (float)min(max(130 - (int)(__float_as_uint(smax) >> 23), -100), 60);
-        const float lv_new = step_limit == 0u ? fit : fminf(lv, fit);
-        float alpha = 0.f;
-        if (m_run != -INFINITY) alpha = ex2_approx((m_run - lv) - ((move ? mx : m_run) - lv_new));
-        if (move) m_run = mx;
-        lv = lv_new;
-        step_limit = (uint32_t)(127 + 7 - (int)lv) << 7;
-        step_limit |= step_limit << 16;
+      for (int w = 0; w < NG / 2; ++w) {
+        ps[w] = bf16x2_mul(ps[w], fac[w]);
+        wide |= bf16x2_any_gt(ps[w], kKv4ScaledMax);
+      }
+      if (__any_sync(0xffffffffu, move || wide)) {
+        const float m_new = move ? mx + kKv4RefAbove : m_run;
+        const float alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
+        m_run = m_new;
         l_part *= alpha;
         const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t4);      // row 2t
         const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);  // row 2t + 1
+        kv4_steps<NG>(at_sw, ps);
+        uint32_t big = NG == 4 ? bf16x2_max(ps[0], ps[NG / 2 - 1]) : ps[0];
+        big = bf16x2_max(big, __byte_perm(big, 0u, 0x1032));
 #pragma unroll
-        for (int c = 0; c < NG; ++c)
+        for (int off = 16; off > 0; off >>= 1) big = bf16x2_max(big, __shfl_xor_sync(0xffffffffu, big, off));
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+        for (int w = 0; w < NG / 2; ++w) {
+          int now[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) oacc[c][k][e] *= (e & 1) ? a1 : a0;
+          for (int h = 0; h < 2; ++h) {
+            const int old = (int)(fac[w] >> (h ? 23 : 7)) & 0xFF;
+            now[h] = min(old, kv4_factor_exp(h ? big >> 16 : big & 0xFFFFu));
+            const float f = __uint_as_float((uint32_t)max(127 + now[h] - old, 0) << 23);
+            const float f0 = a0 * f, f1 = a1 * f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) oacc[2 * w + h][k][e] *= (e & 1) ? f1 : f0;
+          }
+          fac[w] = (uint32_t)now[0] << 7 | (uint32_t)now[1] << 23;
+          ps[w] = bf16x2_mul(ps[w], fac[w]);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) zacc[e] *= (e & 1) ? a1 : a0;
       }
-      const float ref = m_run == -INFINITY ? 0.f : m_run - lv;
+      if constexpr (NG == 4)
+        sts64(at_sw, ps[0], ps[1]);
+      else
+        sts32(at_sw, ps[0]);
+      const float ref = m_run == -INFINITY ? 0.f : m_run;
       float2 pv[2][2];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -799,6 +843,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
       l_part += lsum.x + lsum.y;
 
       // ---- O^T += V^T P^T
+      __syncwarp();  // the scaled steps
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const uint32_t vs = st + off_ks + (C::OFF_VP - C::OFF_KP) + 16 * u * C::PB;
@@ -861,7 +906,7 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
     float l_row = l_part + __shfl_xor_sync(0xffffffffu, l_part, 1);
     l_row += __shfl_xor_sync(0xffffffffu, l_row, 2);
     if (t4 == 0) {
-      m_s[warp * 8 + g] = m_run - lv;
+      m_s[warp * 8 + g] = m_run;
       l_s[warp * 8 + g] = l_row;
     }
 #pragma unroll
@@ -872,12 +917,15 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
         const float add0 = __shfl_sync(0xffffffffu, zacc[0], 4 * zrow + t4);
         const float add1 = __shfl_sync(0xffffffffu, zacc[1], 4 * zrow + t4);
         const int at_d = 32 * c - h * (D / 2) + 4 * g;
+        const float un = __uint_as_float((254u - ((fac[c / 2] >> (c & 1 ? 23 : 7)) & 0xFFu)) << 23);  // 1 / factor
         if (2 * t4 < G)
           *reinterpret_cast<float4*>(&mrg[(warp * G + 2 * t4) * (D / 2) + at_d]) =
-              make_float4(oacc[c][0][0] + add0, oacc[c][0][2] + add0, oacc[c][1][0] + add0, oacc[c][1][2] + add0);
+              make_float4(fmaf(oacc[c][0][0], un, add0), fmaf(oacc[c][0][2], un, add0),
+                          fmaf(oacc[c][1][0], un, add0), fmaf(oacc[c][1][2], un, add0));
         if (2 * t4 + 1 < G)
           *reinterpret_cast<float4*>(&mrg[(warp * G + 2 * t4 + 1) * (D / 2) + at_d]) =
-              make_float4(oacc[c][0][1] + add1, oacc[c][0][3] + add1, oacc[c][1][1] + add1, oacc[c][1][3] + add1);
+              make_float4(fmaf(oacc[c][0][1], un, add1), fmaf(oacc[c][0][3], un, add1),
+                          fmaf(oacc[c][1][1], un, add1), fmaf(oacc[c][1][3], un, add1));
       }
       __syncthreads();
       for (int idx = threadIdx.x; idx < G * (D / 2); idx += C::THREADS) {

@@ -310,3 +310,31 @@ def test_offsets_past_32_bits():
     ref, tol, rl = P.decode(q[-1:], kv, vv, vp, [n], 0, 0, d ** -0.5)
     P.check(o[-1:], ref, tol, "O")
     P.check_lse(lse[-1:], rl)
+
+
+def _appended(k, v):
+    """A cache filled by append from bf16 k, v [1,Hkv,T,d], and its values."""
+    _, Hkv, T, d = k.shape
+    cache = fa.kv4_cache(1, Hkv, T, d)
+    fa.kv4_append(k.transpose(1, 2).contiguous().cuda(), v.transpose(1, 2).contiguous().cuda(), cache, _i32([0]))
+    return cache, P.values4(cache.k_codes, cache.k_params)[0], P.values4(cache.v_codes, cache.v_params)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("first", [
+    # values of V in the first half of the keys, those of the second, by group
+    (None, 1.0), (None, 1e30), (1e30, None), (1e-30, 1e30), (1e30, 1e-30), (None, 1e-30), (1e-30, None), (1e33, 1.0)])
+def test_decode_lse_does_not_depend_on_v(d, first):
+    """Constant groups (steps of 0), very small and very large steps one after the
+    other: the denominator and LSE keep every key."""
+    Hkv, Hq, Tk = 1, 8, 704
+    k, v = _rand((1, Hkv, Tk, d), 97), _rand((1, Hkv, Tk, d), 98).float()
+    for x, at in zip(first, (slice(0, 352), slice(352, 704))):
+        v[:, :, at] = 0.75 if x is None else v[:, :, at] * x
+    cache, kv, (vv, vp) = _appended(k, v.to(torch.bfloat16))
+    q = _rand((1, Hq, d), 99)
+    o, lse = fa.kv4_decode(q.cuda(), cache, _i32([700]))
+    assert fa.check() == 0
+    ref, tol, rl = P.decode(q, kv, vv, vp, [700], 0, 0, d ** -0.5)
+    P.check_lse(lse, rl)
+    P.check(o, ref, tol, "O")
