@@ -490,9 +490,10 @@ int fa_kv4_read(void* k, void* v, const void* k_codes, const void* k_params, con
  * Hq/Hkv must be 1, 2, 4 or 8, and B * Hkv * Tk_max at most 2^36.  Rows that the
  * query does not see may hold anything.  The same inputs give the same bits.
  * LSE depends on q and K alone.  q and p times V's step are multiplied as fp16
- * with factors that follow the largest value of the row of q and the largest step
- * of V met so far: V's values whose steps are 2^18 or more below the largest lose
- * bits, and 2^28 below it they keep their centres alone.  A row of q with a value
+ * with factors that follow the largest value of the row of q and, for each group
+ * of V's dims, the largest step met so far: values of that group whose steps are 2^18
+ * or more below it lose bits, and 2^28 below it they keep their centres alone.  A
+ * NaN, an infinity or a very large value in a visible row of V stays with its group.  A row of q with a value
  * of 2^118 or more comes out non-finite.  K and V of magnitudes below 2^96 stay in
  * range whatever the number of keys.
  */

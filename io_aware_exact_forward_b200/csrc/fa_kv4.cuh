@@ -306,10 +306,11 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
 // reference of the exponentials is 16 above the maximum, so that sums of p times
 // large centres have room).  It is lowered when a step eight times as large comes,
 // and the sums of the codes' part with it; m, l and the centres' part, and so the
-// log-sum-exp, do not depend on it. A p s that is 2^18
+// log-sum-exp, do not depend on it.  Each group of the dims has its own, so that an
+// infinity or a very large value in one leaves the others as they are.  A p s that is 2^18
 // below the largest possible loses bits and one 2^28 below it is dropped: that is p
-// itself, or a key whose steps are that much smaller than others that the same warp
-// has met.  A slice's steps are scaled where they lie in shared
+// itself, or a key whose step is that much smaller than others of its group that
+// the same warp has met.  A slice's steps are scaled where they lie in shared
 // memory, a key by each lane (four instructions a slice; as factors on the
 // probabilities they would be sixteen).
 //
@@ -804,12 +805,11 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
         const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t4);      // row 2t
         const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t4 + 4);  // row 2t + 1
         kv4_steps<NG>(at_sw, ps);
-        uint32_t big = NG == 4 ? bf16x2_max(ps[0], ps[NG / 2 - 1]) : ps[0];
-        big = bf16x2_max(big, __byte_perm(big, 0u, 0x1032));
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) big = bf16x2_max(big, __shfl_xor_sync(0xffffffffu, big, off));
 #pragma unroll
         for (int w = 0; w < NG / 2; ++w) {
+          uint32_t big = ps[w];
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) big = bf16x2_max(big, __shfl_xor_sync(0xffffffffu, big, off));
           int now[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {

@@ -338,3 +338,29 @@ def test_decode_lse_does_not_depend_on_v(d, first):
     ref, tol, rl = P.decode(q, kv, vv, vp, [700], 0, 0, d ** -0.5)
     P.check_lse(lse, rl)
     P.check(o, ref, tol, "O")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("key", [3, 500])
+@pytest.mark.parametrize("x", [float("inf"), float("-inf"), float("nan"), 3e38, 1e30, -1e12])
+def test_decode_keeps_a_group_s_values_to_itself(d, key, x):
+    """An infinity, a NaN or a very large value in one group of a visible row of
+    V: the other groups of that head are as without it."""
+    Hkv, Hq, Tk, g = 2, 8, 704, 1
+    k, v = _rand((1, Hkv, Tk, d), 100), _rand((1, Hkv, Tk, d), 101)
+    v[0, 1, key, 32 * g + 7] = x
+    cache, kv, (vv, vp) = _appended(k, v)
+    q = _rand((1, Hq, d), 102)
+    o, lse = fa.kv4_decode(q.cuda(), cache, _i32([700]))
+    assert fa.check() == 0
+    hit = torch.zeros(1, Hq, d, dtype=torch.bool)
+    hit[0, Hq // 2:, 32 * g:32 * g + 32] = True
+    if abs(x) < float("inf"):
+        ref, tol, rl = P.decode(q, kv, vv, vp, [700], 0, 0, d ** -0.5)
+        P.check(o, ref, tol, "O")
+    else:
+        assert not bool(torch.isfinite(o.cpu()[hit]).any())
+        vv[0, 1, key, 32 * g:32 * g + 32] = vp[0, 1, key, 32 * g:32 * g + 32] = 0
+        ref, tol, rl = P.decode(q, kv, vv, vp, [700], 0, 0, d ** -0.5)
+        P.check(o.cpu()[~hit], ref[~hit], tol[~hit], "O")
+    P.check_lse(lse, rl)
