@@ -219,7 +219,9 @@ int fa_backward_deterministic(const void* q, const void* k, const void* v, const
  *                  its own as fa_backward_deterministic.
  *   ws             at least fa_backward_sinks_workspace_bytes(): the workspace of
  *                  fa_backward and the pieces' partial sums.
- * Other arguments and errors as fa_backward_window.
+ * Probabilities of any size count, however far a sink's score lies above the
+ * others.  Products dO V and D have to stay below 2^112.  Other arguments and
+ * errors as fa_backward_window.
  */
 size_t fa_backward_sinks_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d, int window, int sinks);
 int fa_backward_sinks(const void* q, const void* k, const void* v, const void* o,

@@ -428,7 +428,8 @@ size_t fa_backward_sinks_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk,
 // zero_acc = false leaves the fp32 dQ accumulator alone (a backward whose dQ
 // pass writes dq directly does not read it).
 static int preprocess_impl(const void* o, const float* lse, const void* dO, void* ws, size_t ws_bytes, int B,
-                           int Hq, int Hkv, int Tq, int Tk, int d, void* stream, bool zero_acc) {
+                           int Hq, int Hkv, int Tq, int Tk, int d, void* stream, bool zero_acc,
+                           float p_log2 = 0.f) {
   int st = check_prefill(B, Hq, Hkv, Tq, Tk, d, 1.f, 0);
   if (st) return st;
   if (B == 0 || Tq == 0) return FA_OK;
@@ -444,9 +445,9 @@ static int preprocess_impl(const void* o, const float* lse, const void* dO, void
   const __nv_bfloat16* do16 = reinterpret_cast<const __nv_bfloat16*>(dO);
   float* acc = zero_acc ? w.dq_acc : nullptr;
   if (d == 64)
-    fa_bwd_preprocess_kernel<64><<<blocks, 256, 0, s>>>(o16, do16, lse, w.Dv, w.lse2, acc, B, Hq, Tq, Tp);
+    fa_bwd_preprocess_kernel<64><<<blocks, 256, 0, s>>>(o16, do16, lse, w.Dv, w.lse2, acc, B, Hq, Tq, Tp, p_log2);
   else
-    fa_bwd_preprocess_kernel<128><<<blocks, 256, 0, s>>>(o16, do16, lse, w.Dv, w.lse2, acc, B, Hq, Tq, Tp);
+    fa_bwd_preprocess_kernel<128><<<blocks, 256, 0, s>>>(o16, do16, lse, w.Dv, w.lse2, acc, B, Hq, Tq, Tp, p_log2);
   return launch_status();
 }
 
@@ -494,7 +495,8 @@ static int dkdv_impl(const void* q, const void* k, const void* v, const void* dO
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Tq = Tq; p.Tk = Tk; p.causal = causal;
   p.window = window;
   p.Tq_pad = tq_pad(Tq);
-  p.scale = scale;
+  p.dv_scale = sinks > 0 ? exp2f(-SINK_P_LOG2) : 1.f;
+  p.scale = scale * p.dv_scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.n_kv_tiles = (Tk + 127) / 128;
   p.n_items = p.n_kv_tiles * B * Hkv;
@@ -596,7 +598,7 @@ static int dkdv_impl(const void* q, const void* k, const void* v, const void* dO
   qp.window = window;
   qp.sinks = sinks;
   qp.Tq_pad = p.Tq_pad;
-  qp.scale = scale;
+  qp.scale = p.scale;
   qp.scale_log2 = p.scale_log2;
   qp.n_qt = (Tq + 127) / 128;
   const long long n_items = (long long)B * Hq * qp.n_qt;
@@ -679,7 +681,9 @@ static int backward_impl(const void* q, const void* k, const void* v, const void
   // deterministic: the dQ pass writes dq itself (when there are keys; with
   // none, dq is the zeroed accumulator converted)
   const bool direct = det && Tq > 0 && Tk > 0;
-  if ((st = preprocess_impl(o, lse, dO, ws, ws_bytes, B, Hq, Hkv, Tq, Tk, d, stream, !direct))) return st;
+  if ((st = preprocess_impl(o, lse, dO, ws, ws_bytes, B, Hq, Hkv, Tq, Tk, d, stream, !direct,
+                            sinks > 0 ? (float)SINK_P_LOG2 : 0.f)))
+    return st;
   if ((st = dkdv_impl(q, k, v, dO, dk, dv, ws, ws_bytes, B, Hq, Hkv, Tq, Tk, d, scale, causal, window, stream,
                       drop_t, seed_lo, seed_hi, drop_offset, det, direct ? dq : nullptr, sinks)))
     return st;

@@ -33,11 +33,14 @@
 //                With sinks P^T is kept twice in the S^T columns, in bf16 for
 //                dV's product and in fp16 for the dS warps: dS is then rounded
 //                to bf16 once, not twice (error of dQ and dK 0.0025 of their
-//                norm against 0.0030, at no cost in time).  The key tiles that
+//                norm against 0.0030).  P carries a factor of 2^14 (SINK_P_LOG2),
+//                so that fp16 holds it to 2^-28 in full; where a key's P are all
+//                smaller, as beside a sink that takes the rows' weight, a warp's
+//                part of the tile goes to the dS warps in bf16.  The key tiles that
 //                hold sinks are seen by every later query tile; they are cut
 //                into pieces along the queries so that no item outlasts the
-//                others (T = 8192, W = 1024: 556 us in all for the backward,
-//                584 TFLOP/s of visible pairs).
+//                others (T = 8192, W = 1024: 557 us in all for the backward,
+//                580 TFLOP/s of visible pairs).
 //                dQ_tile is read by a second warpgroup, staged in shared
 //                memory and added into an fp32 accumulator in global memory
 //                with bulk tensor reduce-adds (every KV tile contributes to
@@ -53,7 +56,7 @@
 // product, warps 16-19 idle) and takes dQ from the pass in fa_bwd_dq.cuh.
 #pragma once
 
-#include <cuda_fp16.h>
+#include <type_traits>
 
 #include "fa_ptx.cuh"
 
@@ -64,12 +67,13 @@ namespace fa {
 // ---------------------------------------------------------------------------
 // Dv and lse2 rows have a pitch of Tq_pad = Tq rounded up to 128, so that
 // every 128-row slice starts 16-byte aligned for a bulk copy; the padding
-// entries hold D = 0 and LSE2 = +inf (P = 0).
+// entries hold D = 0 and LSE2 = +inf (P = 0).  p_log2 is taken off LSE2: P then
+// carries a factor of 2^p_log2.
 template <int D>
 __global__ void __launch_bounds__(256) fa_bwd_preprocess_kernel(
     const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dO,
     const float* __restrict__ lse, float* __restrict__ Dv, float* __restrict__ lse2,
-    float* __restrict__ dq_acc, int B, int Hq, int Tq, int Tq_pad) {
+    float* __restrict__ dq_acc, int B, int Hq, int Tq, int Tq_pad, float p_log2) {
   constexpr int LPR = D / 8;  // lanes per row, 8 elements (16 bytes) each
   const long long gid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long row = gid / LPR;            // row index in [B][Tq][Hq] order
@@ -104,7 +108,7 @@ __global__ void __launch_bounds__(256) fa_bwd_preprocess_kernel(
     const long long bh = (long long)b * Hq + h;
     Dv[bh * Tq_pad + t] = dot;
     const float l = lse[bh * Tq + t];
-    lse2[bh * Tq_pad + t] = (l == -INFINITY) ? INFINITY : l * 1.4426950408889634f;
+    lse2[bh * Tq_pad + t] = (l == -INFINITY) ? INFINITY : fmaf(l, 1.4426950408889634f, -p_log2);
   }
   const int npad = Tq_pad - Tq;
   if (npad > 0 && gid < (long long)B * Hq * npad) {
@@ -136,10 +140,10 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_convert_kernel(const float* __r
 // ---------------------------------------------------------------------------
 // dK / dV (+ dQ contributions)
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
+// With sinks LSE2 is stored less 14, which gives P, and with it dS, dV, dK and dQ, a
+// factor of 2^14 that the results' factors take away again.  P is at most 1 but for
+// the roundings of its exponent, for which fp16's 65504 leaves a factor of 4.
+static constexpr int SINK_P_LOG2 = 14;
 
 struct BwdParams {
   CUtensorMap tm_q;    // [B][Tq][Hq][d] bf16, box {64,1,128,1}, 128-byte swizzle
@@ -163,7 +167,8 @@ struct BwdParams {
   int sinks, n_sink_tiles, pieces;
   float* sink_part;
   int Tq_pad;          // row pitch of lse2 / Dv
-  float scale, scale_log2;
+  float scale, scale_log2;  // of dK and dQ (less P's factor), of the scores
+  float dv_scale;           // of dV
   int n_kv_tiles;
   int n_items;         // n_kv_tiles * B * Hkv
   // dropout on P (the DROP instantiation): keep iff the Philox byte < drop_t
@@ -766,6 +771,7 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
         // overlaps the exponentials of chunk c.  P^T (bf16 pairs) goes to
         // the first 32 columns of this warp's 64, never ahead of its loads.
         uint32_t sv[2][16];
+        uint32_t any = 0u;  // sinks: the bits that any of this key's fp16 P has (chunks 0 and 3)
         tmem_ld16(tS, sv[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -793,8 +799,10 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
             if constexpr (WIN == 2) ph[e] = pack_f16x2(p0, p1);
           }
           if constexpr (WIN == 2) {
-            // P is at most 1, so fp16 holds it to 2^-12 of itself (2^-25 below
-            // 2^-14): dS = P (dP - D) is then rounded to bf16 once, not twice
+            if (c == 0 || c == 3) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) any |= ph[e];
+            }
             tmem_st8(tS + c * 16 + 8, ph);
             tmem_st8(tS + c * 16, pk);
           } else if constexpr (DROP) {
@@ -811,6 +819,26 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
           }
         }
         tmem_wait_st();
+        if constexpr (WIN == 2) {
+          // A key that is visible, but to no query with a P of 2^-21 or more (the
+          // fp16 copy's exponents 8 and up): this warp's P goes to the dS warps in
+          // bf16, which the sign, of no use otherwise, tells them.  Beside a P of
+          // 2^-21 what fp16 loses, 2^-39, is nothing to the key's gradients.  Looked at
+          // are the first and last 16 columns, of which a masked key sees some.
+          const bool small = !(any & 0x60006000u) && (masked ? (seen[0] | seen[1]) != 0u : true);
+          if (__any_sync(0xffffffffu, small)) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[8];
+              tmem_ld8(tS + c * 16, pk);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) pk[e] |= 0x80008000u;
+              tmem_st8(tS + c * 16 + 8, pk);
+            }
+            tmem_wait_st();
+          }
+        }
         tc_fence_before();
         mbar_arrive(bar_p_full(buf));
       }
@@ -825,7 +853,7 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         const uint32_t tsrc = tmem + (which ? C::TM_DK : C::TM_DV) + lane_off + half * (D / 2);
-        const float mul = which ? p.scale : (DROP ? p.drop_scale : 1.f);
+        const float mul = which ? p.scale : WIN == 2 ? p.dv_scale : (DROP ? p.drop_scale : 1.f);
         __nv_bfloat16* dst = (which ? p.dk : p.dv) +
                              (((size_t)I.b * p.Tk + (key < p.Tk ? key : 0)) * p.Hkv + I.hkv) * D + half * (D / 2);
 #pragma unroll
@@ -930,57 +958,69 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
         if (!ok) break;
         tc_fence_after();
         const float* drow = dd_s + s * 128 + 64 * half;
-        // Four chunks of 16 query columns; dS overwrites P in pp.
+        // Four chunks of 16 query columns; dS overwrites P in pp.  P_FMT 0: bf16; 1:
+        // fp16; 2: bf16 with the signs set.
+        auto chunks = [&](auto fmt) {
+          constexpr int P_FMT = decltype(fmt)::value;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t dp[16];
-          tmem_ld16(tDP + 16 * c, dp);
-          tmem_wait_ld();
-          if (c == 3) {
-            // every dP^T column of this warp has been read
-            tc_fence_before();
-            mbar_arrive(bar_dp_free);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float2 pf;
-            if constexpr (WIN == 2)
-              pf = __half22float2(*reinterpret_cast<const __half2*>(&pp[8 * c + e]));
-            else
-              pf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&pp[8 * c + e]));
-            const float2 dd = *reinterpret_cast<const float2*>(drow + 16 * c + 2 * e);
-            float2 t;
-            if constexpr (DROP) {
-              // Z * s * dP - D
-              const uint32_t kb = keep[c >> 1] >> (16 * (c & 1) + 2 * e);
-              const float2 zs = make_float2(kb & 1u ? p.drop_scale : 0.f, kb & 2u ? p.drop_scale : 0.f);
-              t = __ffma2_rn(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), zs,
-                             make_float2(-dd.x, -dd.y));
-            } else {
-              t = __fadd2_rn(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])),
-                             make_float2(-dd.x, -dd.y));
+          for (int c = 0; c < 4; ++c) {
+            uint32_t dp[16];
+            tmem_ld16(tDP + 16 * c, dp);
+            tmem_wait_ld();
+            if (c == 3) {
+              // every dP^T column of this warp has been read
+              tc_fence_before();
+              mbar_arrive(bar_dp_free);
             }
-            const float2 r = __fmul2_rn(pf, t);
-            pp[8 * c + e] = pack_bf16x2(r.x, r.y);
-          }
-          if (c == 0 && gi > 0) {
-            // The shared dS tile is still an operand of the previous tile's
-            // dK and dQ MMAs until they complete (this tile's dP^T can
-            // complete before them).
-            ok = __all_sync(0xffffffffu,
-                            (D == 64 || !DQ) ? mbar_wait(bar_qdo_empty(stg(gi - 1)), stg_par(gi - 1), wc)
-                                    : mbar_wait(bar_dq_full((gi - 1) % C::NSBUF), ((gi - 1) / C::NSBUF) & 1, wc));
-            if (!ok) break;
-          }
-          // dS into shared memory: row j of box `half`, 16-byte chunks 2c and
-          // 2c+1, 128-byte swizzle (chunk ^ (row % 8)).
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int chunk = 2 * c + q;
-            *reinterpret_cast<uint4*>(ds_row + ((chunk ^ (j & 7)) << 4)) =
-                make_uint4(pp[8 * c + 4 * q], pp[8 * c + 4 * q + 1], pp[8 * c + 4 * q + 2], pp[8 * c + 4 * q + 3]);
+            for (int e = 0; e < 8; ++e) {
+              float2 pf;
+              if constexpr (P_FMT == 1) {
+                pf = __half22float2(*reinterpret_cast<const __half2*>(&pp[8 * c + e]));
+              } else {
+                if constexpr (P_FMT == 2) pp[8 * c + e] &= 0x7FFF7FFFu;
+                pf = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&pp[8 * c + e]));
+              }
+              const float2 dd = *reinterpret_cast<const float2*>(drow + 16 * c + 2 * e);
+              float2 t;
+              if constexpr (DROP) {
+                // Z * s * dP - D
+                const uint32_t kb = keep[c >> 1] >> (16 * (c & 1) + 2 * e);
+                const float2 zs = make_float2(kb & 1u ? p.drop_scale : 0.f, kb & 2u ? p.drop_scale : 0.f);
+                t = __ffma2_rn(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])), zs,
+                               make_float2(-dd.x, -dd.y));
+              } else {
+                t = __fadd2_rn(make_float2(__uint_as_float(dp[2 * e]), __uint_as_float(dp[2 * e + 1])),
+                               make_float2(-dd.x, -dd.y));
+              }
+              const float2 r = __fmul2_rn(pf, t);
+              pp[8 * c + e] = pack_bf16x2(r.x, r.y);
+            }
+            if (c == 0 && gi > 0) {
+              // The shared dS tile is still an operand of the previous tile's
+              // dK and dQ MMAs until they complete (this tile's dP^T can
+              // complete before them).
+              ok = __all_sync(0xffffffffu,
+                              (D == 64 || !DQ) ? mbar_wait(bar_qdo_empty(stg(gi - 1)), stg_par(gi - 1), wc)
+                                      : mbar_wait(bar_dq_full((gi - 1) % C::NSBUF), ((gi - 1) / C::NSBUF) & 1, wc));
+              if (!ok) return;
+            }
+            // dS into shared memory: row j of box `half`, 16-byte chunks 2c and
+            // 2c+1, 128-byte swizzle (chunk ^ (row % 8)).
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int chunk = 2 * c + q;
+              *reinterpret_cast<uint4*>(ds_row + ((chunk ^ (j & 7)) << 4)) =
+                  make_uint4(pp[8 * c + 4 * q], pp[8 * c + 4 * q + 1], pp[8 * c + 4 * q + 2], pp[8 * c + 4 * q + 3]);
+            }
           }
-        }
+        };
+        if constexpr (WIN != 2)
+          chunks(std::integral_constant<int, 0>());
+        else if (pp[0] >> 31)  // the same in all lanes of the warp
+          chunks(std::integral_constant<int, 2>());
+        else
+          chunks(std::integral_constant<int, 1>());
         if (!ok) break;
         fence_proxy_async_smem();
         tc_fence_before();

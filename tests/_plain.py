@@ -180,3 +180,31 @@ def decode(q, k, v, parts, lens, window, sinks, scale):
         o[b], lse[b] = O.reshape(Hq, d), L.reshape(Hq)
         t[b] += ((2 * H + R32) * a + H * O.abs()).reshape(Hq, d)
     return o, t, lse
+
+
+def sink_backward_by_rounding(q, k, v, do, window, sinks, scale):
+    """{name: (gradient, tolerance)} for scores of any size, from the roundings
+    that the kernels make: P to bf16 for dV (H) and, at worst, for dS (H; the
+    deterministic dQ pass does not round it), dS to bf16 (H), the result (H), D =
+    sum dO O from the rounded O.  r bounds what the scores' sums
+    in 32 bits, 128 steps of 2^-24 of their sizes, do to a probability, with
+    2^-20 for the log-sum-exp and the exponential."""
+    Hkv = k.shape[2]
+    Q, K, V, G = (split_heads(x, Hkv) for x in (q, k, v, do))
+    o, _, w, a = attention(Q, K, V, visible(q.shape[1], k.shape[1], window, sinks), scale)
+    r = 2 * 128 * 2.0 ** -24 * float((Q.abs() @ K.abs().transpose(-1, -2)).max()) * scale + 2.0 ** -20
+    n = (q.shape[1] * q.shape[2] // Hkv + k.shape[1]) * 2.0 ** -24   # sums over queries or keys
+    dv, gw = w.transpose(-1, -2) @ G, w.transpose(-1, -2) @ G.abs()
+    tv = (H + r + n) * gw
+    dp, dpa = G @ V.transpose(-1, -2), G.abs() @ V.abs().transpose(-1, -2)
+    D = (G * o).sum(-1, keepdim=True)
+    dD = (G.abs() * ((2 * H + r) * a + H * o.abs())).sum(-1, keepdim=True)
+    ds = w * (dp - D)
+    tds = (2 * H + H * H + r + n) * ds.abs() + 1.01 * w * (dD + 128 * 2.0 ** -24 * dpa)
+    dq, tq = ds @ K * scale, tds @ K.abs() * scale
+    dk, tk = ds.transpose(-1, -2) @ Q * scale, tds.transpose(-1, -2) @ Q.abs() * scale
+    out = {"dq": (join_heads(dq), join_heads(tq + H * (dq.abs() + tq)))}
+    for name, x, t in (("dk", dk, tk), ("dv", dv, tv)):
+        x, t = x.sum(2), t.sum(2)
+        out[name] = (x.transpose(1, 2), (t + H * (x.abs() + t)).transpose(1, 2))
+    return {name: (x, t + 1e-36) for name, (x, t) in out.items()}

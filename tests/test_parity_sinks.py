@@ -274,3 +274,23 @@ def test_sink_training_step_in_a_graph(d):
     assert fa.check() == 0
     for a, b in zip(out, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("deterministic", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("above", [12.0, 16.0, 20.0, 40.0])
+def test_sink_backward_where_the_sink_takes_the_weight(above, d, deterministic):
+    """The sink's score lies far above the window's, as trained sinks' do: the
+    other keys' probabilities are e^-12 to e^-40, and their dK is as exact as any."""
+    B, Hq, Hkv, T, W, S = 1, 2, 1, 600, 128, 1
+    q, k, v, do = _inputs(B, Hq, Hkv, T, T, d, W, S)
+    # the first dim of q is 4, and 0 in every key but the sink's
+    q[..., 0], k[..., 0] = 4.0, 0.0
+    k[:, 0, :, 0] = above * d ** 0.5 / 4.0
+    c = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.forward(*c[:3], window=W, sinks=S)
+    got = fa.backward(*c[:3], o, lse, c[3], window=W, sinks=S, deterministic=deterministic)
+    assert fa.check() == 0
+    ref = P.sink_backward_by_rounding(q, k, v, do, W, S, d ** -0.5)
+    for n, x in zip(("dq", "dk", "dv"), got):
+        P.check(x, *ref[n], n)
