@@ -530,6 +530,13 @@ int fa_selftest_bounded_wait(int limit_us, void* stream);
  */
 int fa_selftest_exp2_poly(const float* x, float* y, int n, void* stream);
 
+/*
+ * fa_selftest_chunk_of -- key / chunk as the decode with sinks forms it, without a
+ * division, on the host: -1 for a key below 0 or a chunk that decode refuses.
+ * Exposed so that the arithmetic can be checked at lengths that no cache here has.
+ */
+int fa_selftest_chunk_of(int key, int chunk);
+
 #ifdef __cplusplus
 }
 #endif

@@ -72,6 +72,7 @@ SIGNATURES = {
     "fa_check": (_c_int, [_vp]),
     "fa_selftest_bounded_wait": (_c_int, [_c_int, _vp]),
     "fa_selftest_exp2_poly": (_c_int, [_vp, _vp, _c_int, _vp]),
+    "fa_selftest_chunk_of": (_c_int, [_c_int, _c_int]),
 }
 
 

@@ -810,7 +810,7 @@ static int decode_impl(const void* q, const void* k_cache, const void* v_cache, 
   p.window = window;
   p.sinks = sinks;
   p.sink_chunks = (sinks + chunk - 1) / chunk;
-  p.inv_chunk = ((1ull << 40) + chunk / 64 - 1) / (chunk / 64);
+  p.inv_chunk = chunk_inverse(chunk);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = kWaitLimitNs;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -965,6 +965,11 @@ extern "C" int fa_selftest_exp2_poly(const float* x, float* y, int n, void* stre
   const int pairs = (n + 1) / 2;
   selftest_exp2_poly_kernel<<<(pairs + 255) / 256, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(x, y, n);
   return launch_status();
+}
+
+extern "C" int fa_selftest_chunk_of(int key, int chunk) {
+  if (key < 0 || chunk < 64 || chunk > 4096 || chunk % 64 != 0) return -1;
+  return (int)div_chunk((unsigned)key, chunk_inverse(chunk));
 }
 
 extern "C" int fa_selftest_bounded_wait(int limit_us, void* stream) {

@@ -47,7 +47,7 @@ struct DecodeParams {
   int window;                // > 0: the query sees only the last `window` keys of its sequence
   int sinks;                 // SINK instantiation: and its first `sinks` keys
   int sink_chunks;           // SINK: ceil(sinks / chunk)
-  unsigned long long inv_chunk;  // SINK: ceil(2^40 / (chunk / 64))
+  unsigned inv_chunk;        // SINK: chunk_inverse(chunk)
   float scale_log2;
   unsigned long long wait_limit_ns;
 };
@@ -108,10 +108,17 @@ __device__ __forceinline__ uint32_t swz_off(int key, int ch) {
 // split kernel wrote.
 __device__ __forceinline__ int clamp_seqlen(const DecodeParams& p, int n) { return min(max(n, 0), p.Tk_max); }
 
-// x / chunk for 0 <= x < 2^31: chunk is 64 m with m <= 64, and n = x / 64 < 2^25
-// makes n * ceil(2^40 / m) exceed n * 2^40 / m by less than 2^40 / m.
-__device__ __forceinline__ int div_chunk(const DecodeParams& p, int x) {
-  return (int)((unsigned long long)(x >> 6) * p.inv_chunk >> 40);
+// x / chunk for any 32-bit x and chunk = 64 m, m = 2 .. 64: with n = x / 64 < 2^26,
+// n ceil(2^32 / m) exceeds n 2^32 / m by less than 2^26 m / m = 2^26, which is at
+// most 2^32 / m, and so does not reach the next multiple.  m = 1, whose inverse
+// does not fit 32 bits, is kept as 0.
+__host__ __device__ __forceinline__ unsigned chunk_inverse(int chunk) {
+  const unsigned long long m = (unsigned)chunk / 64u;
+  return (unsigned)(((1ull << 32) + m - 1) / m);
+}
+__host__ __device__ __forceinline__ unsigned div_chunk(unsigned x, unsigned inverse) {
+  const unsigned n = x >> 6;
+  return inverse == 0u ? n : (unsigned)((unsigned long long)n * inverse >> 32);
 }
 
 // Chunks of a sequence that hold a visible key when sinks stay visible behind
@@ -121,9 +128,9 @@ __device__ __forceinline__ int div_chunk(const DecodeParams& p, int x) {
 struct SinkChunks {
   int n_sink, lo, count;
   __device__ __forceinline__ SinkChunks(const DecodeParams& p, int seqlen) {
-    const int end = div_chunk(p, seqlen + p.chunk - 1);
+    const int end = div_chunk((unsigned)seqlen + p.chunk - 1, p.inv_chunk);
     n_sink = min(end, p.sink_chunks);
-    lo = max(n_sink, div_chunk(p, max(0, seqlen - p.window)));
+    lo = max(n_sink, (int)div_chunk(max(0, seqlen - p.window), p.inv_chunk));
     count = n_sink + max(0, end - lo);
   }
   __device__ __forceinline__ int at(int v) const { return v < n_sink ? v : lo + v - n_sink; }

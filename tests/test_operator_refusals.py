@@ -217,3 +217,17 @@ def test_rope_frequencies():
                 dict(rotary_dim=64, scaling="ntk", factor=2.0, length=8192)):
         with pytest.raises(ValueError):
             fa.rope_frequencies(**bad)
+
+
+def test_chunks_of_the_longest_sequences():
+    """Decode with sinks finds a key's chunk without a division: right for every
+    chunk size up to the longest lengths that the checks let through, and past them."""
+    f = fa.load_library().fa_selftest_chunk_of
+    keys = [0, 1, 63, 64, (1 << 31) - 1]
+    keys += [(1 << e) + x for e in range(7, 31) for x in (-65, -64, -63, -1, 0, 1, 62, 63, 64)]
+    for chunk in range(64, 4097, 64):
+        edges = [chunk * (k // chunk) + x for k in keys for x in (-1, 0, 1)]
+        for key in keys + edges:
+            if 0 <= key < 1 << 31:
+                assert f(key, chunk) == key // chunk, (key, chunk)
+    assert f(-1, 64) == -1 and f(5, 0) == -1 and f(5, 100) == -1 and f(5, 8192) == -1
