@@ -188,6 +188,8 @@ def forward(q, k, v, scale=None, causal=False, out=None, lse=None, window=None, 
         _raise("fa_forward", st)
     elif sinks:
         _check_kv_shapes(q, k, v)
+        _check_out("out", out, q.shape)
+        _check_out("lse", lse, (B, Hq, Tq))
         with _on_device(dev.index):
             st = lib.fa_forward_sinks(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Tq, Tk, d,
                                       float(scale), int(window), int(sinks), _stream_ptr(dev))

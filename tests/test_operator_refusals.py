@@ -231,3 +231,23 @@ def test_chunks_of_the_longest_sequences():
             if 0 <= key < 1 << 31:
                 assert f(key, chunk) == key // chunk, (key, chunk)
     assert f(-1, 64) == -1 and f(5, 0) == -1 and f(5, 100) == -1 and f(5, 8192) == -1
+
+
+@pytest.fixture
+def cuda_tensors():
+    """Tensors that say they are on a CUDA device and have no memory: what a binding
+    does not refuse by itself ends at their data_ptr()."""
+    mode = torch._subclasses.fake_tensor.FakeTensorMode(allow_non_fake_inputs=True)
+    with mode:
+        yield lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device="cuda:0")
+
+
+def test_sink_forward_checks_its_outputs(cuda_tensors):
+    t, f32 = cuda_tensors, torch.float32
+    q, k = t(2, 40, 4, 64), t(2, 50, 2, 64)
+    for out in (t(2, 39, 4, 64), t(1, 40, 4, 64), t(2, 40, 4, 32), t(2, 40, 256)):
+        with pytest.raises(ValueError, match="out must have shape"):
+            fa.forward(q, k, k, window=8, sinks=2, out=out)
+    for lse in (t(2, 4, 39, dtype=f32), t(1, 4, 40, dtype=f32), t(2, 40, 4, dtype=f32), t(4, dtype=f32)):
+        with pytest.raises(ValueError, match="lse must have shape"):
+            fa.forward(q, k, k, window=8, sinks=2, lse=lse)
