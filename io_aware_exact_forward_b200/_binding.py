@@ -182,6 +182,8 @@ def forward(q, k, v, scale=None, causal=False, out=None, lse=None, window=None, 
         lse = torch.empty((B, Hq, Tq), dtype=torch.float32, device=dev)
     _check_dev("out", out, torch.bfloat16, dev)
     _check_dev("lse", lse, torch.float32, dev)
+    if not sinks:
+        _check_rooms(q, k, v, out, lse)
     if window is None:
         st = lib.fa_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Tq, Tk, d,
                             float(scale), int(bool(causal)), _stream_ptr(dev))
@@ -210,6 +212,22 @@ def _check_kv_shapes(q, k, v):
 def _check_out(name, t, shape):
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _check_room(name, t, like, n=None):
+    """That t, of whatever shape, holds the n elements that the call reads or writes there."""
+    n = like.numel() if n is None else n
+    if t.numel() < n:
+        raise ValueError(f"{name} has {t.numel()} elements, the call needs {n}")
+
+
+def _check_rooms(q, k, v, out, lse):
+    """Sizes of a prefill call's tensors (their shapes are the caller's: an output may
+    be flattened, or a longer buffer)."""
+    _check_room("k", k, k, q.shape[0] * k.shape[1] * k.shape[2] * q.shape[3])
+    _check_room("v", v, v, q.shape[0] * k.shape[1] * k.shape[2] * q.shape[3])
+    _check_room("out", out, q)
+    _check_room("lse", lse, lse, q.shape[0] * q.shape[1] * q.shape[2])
 
 
 def forward_dropout(q, k, v, p_drop, seed, offset=0, scale=None, causal=False, out=None, lse=None):
@@ -293,12 +311,18 @@ def backward(q, k, v, o, lse, do, scale=None, causal=False, workspace=None, dq=N
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
+    _check_dev("workspace", workspace, torch.uint8 if sinks else workspace.dtype, dev)
+    for n, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+        _check_dev(n, t, torch.bfloat16, dev)
+    if not sinks:
+        _check_rooms(q, k, v, o, lse)
+        for n, t, like in (("do", do, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, k)):
+            _check_room(n, t, like)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk), _ptr(dv),
             _ptr(workspace), workspace.numel(), B, Hq, Hkv, Tq, Tk, d, float(scale))
     if sinks:
         _check_kv_shapes(q, k, v)
         for n, t, like in (("o", o, q), ("do", do, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-            _check_dev(n, t, torch.bfloat16, dev)
             _check_out(n, t, like.shape)
         _check_out("lse", lse, (B, Hq, Tq))
         with _on_device(dev.index):

@@ -251,3 +251,31 @@ def test_sink_forward_checks_its_outputs(cuda_tensors):
     for lse in (t(2, 4, 39, dtype=f32), t(1, 4, 40, dtype=f32), t(2, 40, 4, dtype=f32), t(4, dtype=f32)):
         with pytest.raises(ValueError, match="lse must have shape"):
             fa.forward(q, k, k, window=8, sinks=2, lse=lse)
+
+
+def test_prefill_calls_refuse_short_buffers(cuda_tensors):
+    """forward() and backward() without sinks: what does not hold the elements that the
+    kernels read or write, or is elsewhere, is refused; shapes stay the caller's."""
+    t, f32 = cuda_tensors, torch.float32
+    q, k, o, lse = t(2, 40, 4, 64), t(2, 50, 2, 64), t(2, 40, 4, 64), t(2, 4, 40, dtype=f32)
+    for kw in (dict(out=t(2, 39, 4, 64)), dict(lse=t(2, 4, 39, dtype=f32)), dict(v=t(2, 49, 2, 64)),
+               dict(k=t(1, 50, 2, 64))):
+        for mask in (dict(), dict(causal=True), dict(window=8)):
+            a = dict(dict(q=q, k=k, v=k), **kw)
+            with pytest.raises(ValueError, match="the call needs"):
+                fa.forward(a.pop("q"), a.pop("k"), a.pop("v"), **a, **mask)
+    ws = t(1 << 20, dtype=torch.uint8)
+    short = dict(dq=t(2, 39, 4, 64), dk=t(2, 49, 2, 64), dv=t(2, 49, 2, 64))
+    for n, x in short.items():
+        for mask in (dict(), dict(deterministic=True), dict(window=8)):
+            with pytest.raises(ValueError, match="the call needs"):
+                fa.backward(q, k, k, o, lse, o, workspace=ws, **{n: x}, **mask)
+    with pytest.raises(ValueError, match="the call needs"):
+        fa.backward(q, k, k, o, t(2, 4, 39, dtype=f32), o, workspace=ws)
+    with pytest.raises(ValueError, match="the call needs"):
+        fa.backward(q, k, k, o, lse, t(2, 39, 4, 64), workspace=ws)
+    with pytest.raises(ValueError, match="must be on a CUDA device"):
+        fa.backward(q, k, k, o, lse, o, workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cpu"))
+    for sinks in (dict(), dict(window=8, sinks=2)):
+        with pytest.raises(TypeError, match="dq must be"):
+            fa.backward(q, k, k, o, lse, o, workspace=ws, dq=t(2, 40, 4, 64, dtype=f32), **sinks)
