@@ -281,7 +281,12 @@ def forward_fp8(q, k, v, q_descale, k_descale, v_descale, scale=None, causal=Fal
     return out, lse
 
 
-def backward_workspace_bytes(B, Hq, Hkv, Tq, Tk, d) -> int:
+def backward_workspace_bytes(B, Hq, Hkv, Tq, Tk, d, window=None, sinks=0) -> int:
+    """Bytes that backward() needs as its workspace; with ``sinks``, of that window, more
+    than without."""
+    _need_window(window, sinks)
+    if sinks:
+        return int(load_library().fa_backward_sinks_workspace_bytes(B, Hq, Hkv, Tq, Tk, d, int(window), int(sinks)))
     return int(load_library().fa_backward_workspace_bytes(B, Hq, Hkv, Tq, Tk, d))
 
 
@@ -302,11 +307,8 @@ def backward(q, k, v, o, lse, do, scale=None, causal=False, workspace=None, dq=N
     _check_dev("lse", lse, torch.float32, dev)
     if scale is None:
         scale = d ** -0.5
-    if sinks:
-        need = int(lib.fa_backward_sinks_workspace_bytes(B, Hq, Hkv, Tq, Tk, d, int(window), int(sinks)))
-    else:
-        need = backward_workspace_bytes(B, Hq, Hkv, Tq, Tk, d)
     if workspace is None:
+        need = backward_workspace_bytes(B, Hq, Hkv, Tq, Tk, d, window, sinks)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
@@ -369,7 +371,12 @@ def backward_dropout(q, k, v, o, lse, do, p_drop, seed, offset=0, scale=None, ca
     return dq, dk, dv
 
 
-def decode_workspace_bytes(B, Hq, Tk_max, d, chunk=256) -> int:
+def decode_workspace_bytes(B, Hq, Tk_max, d, chunk=256, window=None, sinks=0) -> int:
+    """Bytes that decode_splitkv() needs as its workspace; with ``sinks``, of that window,
+    as many or fewer."""
+    _need_window(window, sinks)
+    if sinks:
+        return int(load_library().fa_decode_sinks_workspace_bytes(B, Hq, Tk_max, d, chunk, int(window), int(sinks)))
     return int(load_library().fa_decode_workspace_bytes(B, Hq, Tk_max, d, chunk))
 
 

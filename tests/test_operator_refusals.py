@@ -279,3 +279,17 @@ def test_prefill_calls_refuse_short_buffers(cuda_tensors):
     for sinks in (dict(), dict(window=8, sinks=2)):
         with pytest.raises(TypeError, match="dq must be"):
             fa.backward(q, k, k, o, lse, o, workspace=ws, dq=t(2, 40, 4, 64, dtype=f32), **sinks)
+
+
+def test_workspace_sizes_with_sinks():
+    lib = fa.load_library()
+    sizes = (1, 4, 2, 4096, 4096, 64)
+    assert fa.backward_workspace_bytes(*sizes, window=256, sinks=4) == \
+        lib.fa_backward_sinks_workspace_bytes(*sizes, 256, 4) > fa.backward_workspace_bytes(*sizes)
+    assert fa.backward_workspace_bytes(*sizes, window=256) == lib.fa_backward_workspace_bytes(*sizes)
+    sizes = (2, 8, 4096, 128, 256)
+    assert fa.decode_workspace_bytes(*sizes, window=300, sinks=4) == \
+        lib.fa_decode_sinks_workspace_bytes(*sizes, 300, 4) < fa.decode_workspace_bytes(*sizes)
+    for f, s in ((fa.backward_workspace_bytes, (1, 4, 2, 16, 16, 64)), (fa.decode_workspace_bytes, sizes)):
+        with pytest.raises(ValueError, match="window"):
+            f(*s, sinks=4)

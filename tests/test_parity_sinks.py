@@ -294,3 +294,30 @@ def test_sink_backward_where_the_sink_takes_the_weight(above, d, deterministic):
     ref = P.sink_backward_by_rounding(q, k, v, do, W, S, d ** -0.5)
     for n, x in zip(("dq", "dk", "dv"), got):
         P.check(x, *ref[n], n)
+
+
+@pytest.mark.parametrize("deterministic", [False, True])
+def test_sink_workspaces_as_asked_for(deterministic):
+    """Workspaces of just the sizes that the library names: the same results, nothing
+    written behind them, and one byte less is refused."""
+    T, W, S, d = 1500, 64, 200, 64
+    q, k, v, do = (x.cuda() for x in _inputs(1, 4, 2, T, T, d, W, S))
+    o, lse = fa.forward(q, k, v, window=W, sinks=S)
+    need = fa.backward_workspace_bytes(1, 4, 2, T, T, d, window=W, sinks=S)
+    ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    kw = dict(window=W, sinks=S, deterministic=deterministic)
+    want = fa.backward(q, k, v, o, lse, do, **kw)
+    got = fa.backward(q, k, v, o, lse, do, workspace=ws[:need], **kw)
+    assert bool((ws[need:] == 0x5A).all())
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])     # dQ's order is free by default
+    with pytest.raises(fa.FAError):
+        fa.backward(q, k, v, o, lse, do, workspace=ws[:need - 1], **kw)
+    lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+    need = fa.decode_workspace_bytes(1, 4, T, d, window=W, sinks=S)
+    ws.fill_(0x5A)
+    a = fa.decode_splitkv(q[:, -1].contiguous(), k, v, lens, window=W, sinks=S)
+    b = fa.decode_splitkv(q[:, -1].contiguous(), k, v, lens, window=W, sinks=S, workspace=ws[:need])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and bool((ws[need:] == 0x5A).all())
+    with pytest.raises(fa.FAError):
+        fa.decode_splitkv(q[:, -1].contiguous(), k, v, lens, window=W, sinks=S, workspace=ws[:need - 1])
+    assert fa.check() == 0
