@@ -218,7 +218,8 @@ int fa_backward_deterministic(const void* q, const void* k, const void* v, const
  *   deterministic  0: dQ by bulk reduce-adds as fa_backward; 1: dQ in a pass of
  *                  its own as fa_backward_deterministic.
  *   ws             at least fa_backward_sinks_workspace_bytes(): the workspace of
- *                  fa_backward and the pieces' partial sums.
+ *                  fa_backward and the pieces' partial sums, at most another
+ *                  2 B Tq Hq d floats.
  * Probabilities of any size count, however far a sink's score lies above the
  * others.  Products dO V and D have to stay below 2^112.  Other arguments and
  * errors as fa_backward_window.

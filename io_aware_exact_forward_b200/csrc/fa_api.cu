@@ -403,26 +403,30 @@ static int check_ptrs(std::initializer_list<const void*> ptrs) {
 
 // How the backward cuts up the key tiles that hold sinks (see BwdParams): a
 // piece is about as many query tiles as a windowed key tile sees, so that no
-// item outlasts the others by far; at most 32 pieces, so that the partial sums
-// stay small beside the fp32 dQ accumulator.
+// item outlasts the others by far; at most 32 pieces, and no more than keep the
+// partial sums within twice the fp32 dQ accumulator's bytes (with pieces of four
+// query tiles they are half of its bytes per sink tile, divided by the query heads
+// per KV head: several sink tiles have that many more items without being cut so fine).
 struct SinkPlan {
   int tiles, pieces;
   size_t part_bytes;
 };
-static SinkPlan sink_plan(int B, int Hkv, int Tq, int Tk, int d, int window, int sinks) {
+static SinkPlan sink_plan(int B, int Hq, int Hkv, int Tq, int Tk, int d, int window, int sinks) {
   SinkPlan s;
   s.tiles = (std::min(sinks, Tk) + 127) / 128;
   const int n_qt = (Tq + 127) / 128;
   const int per = std::max(4, (int)(((long long)window + 127) / 128) + 1);
-  s.pieces = std::min(32, std::max(1, (n_qt + per - 1) / per));
-  s.part_bytes = s.pieces > 1 ? round256((size_t)B * Hkv * s.tiles * s.pieces * 2 * 128 * d * 4) : 0;
+  const size_t piece_bytes = (size_t)B * Hkv * s.tiles * 2 * 128 * d * 4, acc_bytes = (size_t)B * Tq * Hq * d * 4;
+  const int most = piece_bytes > 0 ? (int)std::min<size_t>(32, 2 * acc_bytes / piece_bytes) : 1;
+  s.pieces = std::max(1, std::min(most, (n_qt + per - 1) / per));
+  s.part_bytes = s.pieces > 1 ? round256(piece_bytes * s.pieces) : 0;
   return s;
 }
 
 size_t fa_backward_sinks_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d, int window, int sinks) {
   const size_t base = fa_backward_workspace_bytes(B, Hq, Hkv, Tq, Tk, d);
   if (base == 0 || Hkv < 1 || Tk < 0 || window < 1 || sinks < 0 || sinks > kMaxSinks) return base;
-  return base + sink_plan(B, Hkv, Tq, Tk, d, window, sinks).part_bytes;
+  return base + sink_plan(B, Hq, Hkv, Tq, Tk, d, window, sinks).part_bytes;
 }
 
 // zero_acc = false leaves the fp32 dQ accumulator alone (a backward whose dQ
@@ -501,7 +505,7 @@ static int dkdv_impl(const void* q, const void* k, const void* v, const void* dO
   p.n_kv_tiles = (Tk + 127) / 128;
   p.n_items = p.n_kv_tiles * B * Hkv;
   if (sinks > 0) {
-    const SinkPlan sp = sink_plan(B, Hkv, Tq, Tk, d, window, sinks);
+    const SinkPlan sp = sink_plan(B, Hq, Hkv, Tq, Tk, d, window, sinks);
     if (ws_bytes < fa_backward_sinks_workspace_bytes(B, Hq, Hkv, Tq, Tk, d, window, sinks)) return FA_ERR_WORKSPACE;
     const long long items = (long long)B * Hkv * (p.n_kv_tiles + (long long)sp.tiles * (sp.pieces - 1));
     if (items > 0x7FFFFFFFll) return FA_ERR_INVALID_ARG;

@@ -293,3 +293,11 @@ def test_workspace_sizes_with_sinks():
     for f, s in ((fa.backward_workspace_bytes, (1, 4, 2, 16, 16, 64)), (fa.decode_workspace_bytes, sizes)):
         with pytest.raises(ValueError, match="window"):
             f(*s, sinks=4)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,T,d,W,S", [(16, 16, 16, 16384, 64, 256, 1024), (1, 8, 1, 65536, 128, 16, 1024),
+                                             (2, 4, 4, 700, 64, 1, 600), (1, 1, 1, 1 << 20, 64, 64, 129)])
+def test_sink_partial_sums_stay_within_twice_the_accumulator(B, Hq, Hkv, T, d, W, S):
+    base = fa.backward_workspace_bytes(B, Hq, Hkv, T, T, d)
+    more = fa.backward_workspace_bytes(B, Hq, Hkv, T, T, d, window=W, sinks=S) - base
+    assert 0 <= more <= 2 * B * T * Hq * d * 4

@@ -321,3 +321,17 @@ def test_sink_workspaces_as_asked_for(deterministic):
     with pytest.raises(fa.FAError):
         fa.decode_splitkv(q[:, -1].contiguous(), k, v, lens, window=W, sinks=S, workspace=ws[:need - 1])
     assert fa.check() == 0
+
+
+@pytest.mark.parametrize("deterministic", [False, True])
+def test_sink_backward_with_many_sink_tiles(deterministic):
+    """Eight sink tiles, cut into fewer pieces than one would be."""
+    B, Hq, Hkv, T, d, W, S = 1, 1, 1, 2048, 64, 64, 1024
+    q, k, v, do = _inputs(B, Hq, Hkv, T, T, d, W, S)
+    c = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.forward(*c[:3], window=W, sinks=S)
+    got = fa.backward(*c[:3], o, lse, c[3], window=W, sinks=S, deterministic=deterministic)
+    assert fa.check() == 0
+    ref = P.sink_backward(q, k, v, do, W, S, d ** -0.5)
+    for n, x in zip(("dq", "dk", "dv"), got):
+        P.check(x, *ref[n], n)
