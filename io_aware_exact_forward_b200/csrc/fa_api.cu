@@ -1215,14 +1215,16 @@ static int kv4_rows_blocks(Kv4RowsParams* p, int B, int T, int Hkv, int Tk_max, 
   p->T = T;
   p->H = Hkv;
   p->Tk_max = Tk_max;
+  if (Hkv > (1 << 24) || T > (1 << 30)) return FA_ERR_INVALID_ARG;
+  int nsm = 0;
+  if (const int st = sm_count(&nsm)) return st;
   // Eight steps along the tokens where that still leaves four blocks a
   // multiprocessor, fewer where it does not.
-  if (Hkv > (1 << 24) || T > (1 << 30)) return FA_ERR_INVALID_ARG;
   p->heads = Hkv >= 2 ? 2 : 1;
   p->parts = (Hkv + p->heads - 1) / p->heads;
   p->tokens = 256 / (p->heads * (d / 8));
   p->steps = 1;
-  while (p->steps < 8 && (long long)B * (T / (p->tokens * p->steps * 2)) * p->parts >= 4 * 148) p->steps *= 2;
+  while (p->steps < 8 && (long long)B * (T / (p->tokens * p->steps * 2)) * p->parts >= 4 * nsm) p->steps *= 2;
   const long long per_seq = (((long long)T + p->tokens * p->steps - 1) / (p->tokens * p->steps)) * p->parts;
   const long long n = per_seq * B;
   if (n > 0x7FFFFFFFll) return FA_ERR_INVALID_ARG;
