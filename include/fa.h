@@ -104,8 +104,8 @@ int fa_forward_window(const void* q, const void* k, const void* v, void* o, floa
  * stay visible behind the window: query i sees key j iff j <= i + (Tk - Tq)
  * and (j > i + (Tk - Tq) - window or j < sinks).  A model that streams past its
  * window keeps its first tokens this way, because rows put much of their weight
- * on them.  sinks = 0 gives fa_forward_window; sinks outside [0, 1024] is
- * FA_ERR_INVALID_ARG.  Key tiles that hold neither sinks nor any key of a query
+ * on them.  sinks = 0 gives fa_forward_window; sinks outside [0, 1024], and with
+ * sinks > 0 a scale that is not positive, are FA_ERR_INVALID_ARG.  Key tiles that hold neither sinks nor any key of a query
  * tile's windows are not read.  Other arguments and errors as
  * fa_forward_window.  Values of K and V have to be finite where any row of the
  * same 128-row query tile sees them (a masked probability is 0, and 0 times a

@@ -339,6 +339,8 @@ int fa_forward_window(const void* q, const void* k, const void* v, void* o, floa
 int fa_forward_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
                      int Tq, int Tk, int d, float scale, int window, int sinks, void* stream) {
   if (window < 1) return FA_ERR_INVALID_ARG;
+  // unseen scores are masked with -inf, and the maximum taken, before the scaling
+  if (sinks > 0 && !(scale > 0.f)) return FA_ERR_INVALID_ARG;
   return forward_impl(q, k, v, o, lse, B, Hq, Hkv, Tq, Tk, d, scale, 1, window, stream, false, 1.f, 1.f, 256, 0, 0, 0,
                       sinks);
 }

@@ -301,3 +301,11 @@ def test_sink_partial_sums_stay_within_twice_the_accumulator(B, Hq, Hkv, T, d, W
     base = fa.backward_workspace_bytes(B, Hq, Hkv, T, T, d)
     more = fa.backward_workspace_bytes(B, Hq, Hkv, T, T, d, window=W, sinks=S) - base
     assert 0 <= more <= 2 * B * T * Hq * d * 4
+
+
+def test_sink_forward_needs_a_positive_scale():
+    """With a scale of 0 or below, the masked scores would turn the row's sum to NaN."""
+    lib = fa.load_library()
+    for scale in (0.0, -0.0, -0.125, -math.inf, math.inf, math.nan):
+        assert lib.fa_forward_sinks(N, N, N, N, N, 1, 1, 1, 0, 16, 64, scale, 4, 4, N) == INVALID, scale
+    assert lib.fa_forward_sinks(N, N, N, N, N, 1, 1, 1, 0, 16, 64, 1e-3, 4, 4, N) == 0
