@@ -105,11 +105,13 @@ int fa_forward_window(const void* q, const void* k, const void* v, void* o, floa
  * and (j > i + (Tk - Tq) - window or j < sinks).  A model that streams past its
  * window keeps its first tokens this way, because rows put much of their weight
  * on them.  sinks = 0 gives fa_forward_window; sinks outside [0, 1024], and with
- * sinks > 0 a scale that is not positive, are FA_ERR_INVALID_ARG.  Key tiles that hold neither sinks nor any key of a query
- * tile's windows are not read.  Other arguments and errors as
- * fa_forward_window.  Values of K and V have to be finite where any row of the
- * same 128-row query tile sees them (a masked probability is 0, and 0 times a
- * NaN or an infinity of V is NaN), as for the other prefill entry points.
+ * sinks > 0 a scale that is not positive, are FA_ERR_INVALID_ARG.  Key tiles that
+ * hold neither sinks nor any key of the windows of a block of 256 query rows are
+ * not read for it.  Other arguments and errors as fa_forward_window.  V has to be finite in every 128-key tile (of keys 128 n to
+ * 128 n + 127) that holds a key which any row of the same block of 256 query rows
+ * sees: a masked probability is 0, and 0 times a NaN or an infinity of V is NaN, as
+ * for the other prefill entry points.  Other tiles, and K where no row sees it, may
+ * hold anything.
  */
 int fa_forward_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
                      int B, int Hq, int Hkv, int Tq, int Tk, int d, float scale, int window,
@@ -220,6 +222,8 @@ int fa_backward_deterministic(const void* q, const void* k, const void* v, const
  *   ws             at least fa_backward_sinks_workspace_bytes(): the workspace of
  *                  fa_backward and the pieces' partial sums, at most another
  *                  2 B Tq Hq d floats.
+ * K, V, q, dO and o have to be finite in all of every 128-row tile of keys and of
+ * queries between which any pair is visible; other key tiles may hold anything.
  * Probabilities of any size count, however far a sink's score lies above the
  * others.  Products dO V and D have to stay below 2^112.  Other arguments and
  * errors as fa_backward_window.

@@ -335,3 +335,28 @@ def test_sink_backward_with_many_sink_tiles(deterministic):
     ref = P.sink_backward(q, k, v, do, W, S, d ** -0.5)
     for n, x in zip(("dq", "dk", "dv"), got):
         P.check(x, *ref[n], n)
+
+
+@pytest.mark.parametrize("deterministic", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_sink_prefill_does_not_read_behind_the_window(d, deterministic):
+    """The last 256 rows of a long sequence: key tiles between the sinks' and the
+    window's may hold NaN, and K may wherever no row sees it (in the forward)."""
+    Tq, Tk, W, S = 256, 2048, 300, 4
+    q, k, v, do = _inputs(1, 4, 2, Tq, Tk, d, W, S)
+    first = Tk - Tq - W + 1                    # of the window of the first row
+    c = [x.cuda() for x in (q, k, v, do)]
+    for t in c[1:3]:
+        t[:, 128:first // 128 * 128] = float("nan")
+    kn = c[1].clone()
+    kn[:, S:first] = float("nan")
+    o, lse = fa.forward(c[0], kn, c[2], window=W, sinks=S)
+    assert fa.check() == 0
+    ref, tol, rl = P.sink_forward(q, k, v, W, S, d ** -0.5)
+    P.check(o, ref, tol, "O")
+    P.check_lse(lse, rl)
+    got = fa.backward(*c[:3], o, lse, c[3], window=W, sinks=S, deterministic=deterministic)
+    assert fa.check() == 0
+    ref = P.sink_backward(q, k, v, do, W, S, d ** -0.5)
+    for n, x in zip(("dq", "dk", "dv"), got):
+        P.check(x, *ref[n], n)
