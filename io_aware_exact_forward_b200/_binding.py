@@ -128,9 +128,15 @@ def _raise(fn, st):
         raise FAError(fn, st)
 
 
-def _need_window(window, sinks):
+_INT = 1 << 31
+
+
+def _need_window(window, sinks, chunk=0):
     if sinks and window is None:
         raise ValueError("sinks need a window (without one every key is visible)")
+    # a C int would take the low 32 bits of a larger number
+    if not (-_INT <= (window or 0) < _INT and -_INT <= sinks < _INT and -_INT <= chunk < _INT):
+        raise ValueError(f"window, sinks and chunk must fit 32 bits, got {window}, {sinks}, {chunk}")
 
 
 _NO_GUARD = contextlib.nullcontext()
@@ -374,7 +380,7 @@ def backward_dropout(q, k, v, o, lse, do, p_drop, seed, offset=0, scale=None, ca
 def decode_workspace_bytes(B, Hq, Tk_max, d, chunk=256, window=None, sinks=0) -> int:
     """Bytes that decode_splitkv() needs as its workspace; with ``sinks``, of that window,
     as many or fewer."""
-    _need_window(window, sinks)
+    _need_window(window, sinks, chunk)
     if sinks:
         return int(load_library().fa_decode_sinks_workspace_bytes(B, Hq, Tk_max, d, chunk, int(window), int(sinks)))
     return int(load_library().fa_decode_workspace_bytes(B, Hq, Tk_max, d, chunk))
@@ -385,8 +391,8 @@ def decode_splitkv(q, k_cache, v_cache, seqlens, scale=None, chunk=256, workspac
     """Split-KV decode.  q [B,Hq,d], caches [B,Tk_max,Hkv,d] bf16, seqlens int32 [B] (CUDA).
     ``window`` (int >= 1) keeps only the last `window` keys of each sequence, and
     ``sinks`` its first ones with them (fa_decode_splitkv_sinks)."""
+    _need_window(window, sinks, chunk)
     if sinks:
-        _need_window(window, sinks)
         return _decode_sinks(q, k_cache, v_cache, seqlens, scale, chunk, workspace, out, lse, window, sinks)
     lib = load_library()
     B, Hq, d = q.shape

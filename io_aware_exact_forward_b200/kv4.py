@@ -16,7 +16,7 @@ from typing import NamedTuple
 
 import torch
 
-from ._binding import _check_dev, _cuda_index, _demand, _on_device, _raise, _stream_of, load_library
+from ._binding import _check_dev, _cuda_index, _demand, _need_window, _on_device, _raise, _stream_of, load_library
 
 __all__ = ["KV4Cache", "kv4_cache", "kv4_append", "kv4_read", "kv4_decode", "kv4_decode_workspace_bytes"]
 
@@ -142,9 +142,8 @@ def kv4_decode(q, cache, seqlens, scale=None, window=None, sinks=0, workspace=No
     of q [B,Hq,d] against the first seqlens[b] keys (int32 [B]) of each sequence;
     ``window`` and ``sinks`` as in decode_splitkv()."""
     lib = load_library()
+    _need_window(window, sinks)
     if window is None:
-        if sinks:
-            raise ValueError("sinks need a window (without one every key is visible)")
         window = 0
     elif window < 1:
         raise ValueError(f"window must be at least 1, got {window}")

@@ -309,3 +309,28 @@ def test_sink_forward_needs_a_positive_scale():
     for scale in (0.0, -0.0, -0.125, -math.inf, math.inf, math.nan):
         assert lib.fa_forward_sinks(N, N, N, N, N, 1, 1, 1, 0, 16, 64, scale, 4, 4, N) == INVALID, scale
     assert lib.fa_forward_sinks(N, N, N, N, N, 1, 1, 1, 0, 16, 64, 1e-3, 4, 4, N) == 0
+
+
+def test_numbers_past_32_bits_are_refused(cuda_tensors):
+    """Their low 32 bits, which a C int would take, are a window, sinks or a chunk of
+    their own."""
+    t = cuda_tensors
+    q, k, n = t(2, 40, 4, 64), t(2, 64, 2, 64), t(2, dtype=torch.int32)
+    cache = fa.kv4_cache(2, 2, 64, 64, device="cuda:0")
+    big = 1 << 32
+    for kw in (dict(window=big + 8), dict(window=big + 8, sinks=2), dict(window=8, sinks=big + 2),
+               dict(window=-big + 8, sinks=2)):
+        with pytest.raises(ValueError, match="32 bits"):
+            fa.forward(q, k, k, **kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            fa.backward(q, k, k, q, t(2, 4, 40, dtype=torch.float32), q, **kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            fa.decode_splitkv(q[:, 0], k, k, n, **kw)
+        with pytest.raises(ValueError, match="32 bits|at least 1"):
+            fa.kv4_decode(q[:, 0], cache, n, **kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            fa.backward_workspace_bytes(2, 4, 2, 40, 64, 64, **kw)
+    with pytest.raises(ValueError, match="32 bits"):
+        fa.decode_splitkv(q[:, 0], k, k, n, chunk=big + 64)
+    with pytest.raises(ValueError, match="32 bits"):
+        fa.decode_workspace_bytes(2, 4, 64, 64, chunk=big + 64)
