@@ -472,11 +472,12 @@ int fa_rope_backward(const void* dq, void* dq_out, const void* dk, void* dk_out,
  * each >= 0 and a multiple of 8) into the cache at positions start[b] + t.
  *   start  DEVICE int32 [B];  count  DEVICE int32 [B], rows of sequence b that
  *          are written (t < count[b]), or NULL: all T.
- * Rows at positions outside [0, Tk_max) are dropped; nothing else is written.
+ * Rows at positions outside [0, Tk_max) are dropped; nothing else is written.  No
+ * two of the four buffers may share memory.
  *
  * fa_kv4_read -- the values at positions start[b] + t, rounded to bf16, as dense
  * k, v [B,T,Hkv,d] (a prefill's keys, for instance).  Rows t >= count[b], or
- * outside [0, Tk_max), read as zeros.
+ * outside [0, Tk_max), read as zeros.  k and v may not share memory.
  */
 int fa_kv4_append(const void* k, const void* v, const int64_t* strides, void* k_codes, void* k_params,
                   void* v_codes, void* v_params, const int* start, const int* count,

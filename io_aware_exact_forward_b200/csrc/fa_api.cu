@@ -1207,6 +1207,24 @@ static int kv4_check_cache(const void* k_codes, const void* k_params, const void
   return FA_OK;
 }
 
+static bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return a < b ? b - a < nx : a - b < ny;
+}
+
+// Whether any two of a cache's four buffers share memory: K's and V's blocks run
+// in any order.
+static bool kv4_cache_overlaps(const void* k_codes, const void* k_params, const void* v_codes, const void* v_params,
+                               int B, int Hkv, int Tk_max, int d) {
+  const size_t rows = (size_t)B * Hkv * Tk_max;
+  const void* ptr[4] = {k_codes, k_params, v_codes, v_params};
+  const size_t bytes[4] = {rows * (d / 2), rows * (d / 8), rows * (d / 2), rows * (d / 8)};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(ptr[i], bytes[i], ptr[j], bytes[j])) return true;
+  return false;
+}
+
 static int kv4_check_sizes(int B, int Hkv, int Tk_max, int d) {
   if (B < 0 || Hkv < 1 || Tk_max < 0 || Tk_max % 64 != 0 || Tk_max > (1 << 30)) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
@@ -1253,6 +1271,7 @@ extern "C" int fa_kv4_append(const void* k, const void* v, const int64_t* stride
     return FA_ERR_ALIGNMENT;
   for (int i = 0; i < 6; ++i)
     if (strides[i] & 7) return FA_ERR_ALIGNMENT;
+  if (kv4_cache_overlaps(k_codes, k_params, v_codes, v_params, B, Hkv, Tk_max, d)) return FA_ERR_INVALID_ARG;
   Kv4RowsParams p;
   memset(&p, 0, sizeof(p));
   unsigned blocks = 0;
@@ -1291,6 +1310,8 @@ extern "C" int fa_kv4_read(void* k, void* v, const void* k_codes, const void* k_
   if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(start) & 3u) ||
       (reinterpret_cast<uintptr_t>(count) & 3u))
     return FA_ERR_ALIGNMENT;
+  const size_t out_bytes = (size_t)B * T * Hkv * d * 2;
+  if (overlap(k, out_bytes, v, out_bytes)) return FA_ERR_INVALID_ARG;
   Kv4RowsParams p;
   memset(&p, 0, sizeof(p));
   unsigned blocks = 0;

@@ -334,3 +334,28 @@ def test_numbers_past_32_bits_are_refused(cuda_tensors):
         fa.decode_splitkv(q[:, 0], k, k, n, chunk=big + 64)
     with pytest.raises(ValueError, match="32 bits"):
         fa.decode_workspace_bytes(2, 4, 64, 64, chunk=big + 64)
+
+
+def test_kv4_outputs_share_no_memory(mem):
+    """K and V are written by blocks that run in any order."""
+    lib = fa.load_library()
+    st = strides(*(2 * 64, 2 * 64, 64) * 2)
+    p = lambda *x: [mem(v) for v in x]  # noqa: E731
+    codes, params = 2 * 64 * 32, 2 * 64 * 8         # bytes of one buffer, at [1, 2, 64]
+
+    def append(kc, kp, vc, vp):
+        return lib.fa_kv4_append(*p(0, 512), st, *p(kc, kp, vc, vp), mem(256), N, 1, 1, 2, 64, 64, N)
+
+    apart = (0, 2 * codes, codes, 2 * codes + params)
+    for i in range(4):
+        for j in range(4):
+            if i != j:
+                bad = list(apart)
+                bad[i] = bad[j] + 16 * (i > j)
+                assert append(*bad) == INVALID, (i, j)
+    read = lambda k, v, T: lib.fa_kv4_read(*p(k, v), *p(*apart), mem(256), N, 1, T, 2, 64, 64, N)  # noqa: E731
+    assert read(0, 0, 1) == INVALID and read(0, 240, 1) == INVALID and read(1008, 0, 4) == INVALID
+    if not torch.cuda.is_available():
+        # apart: the call gets as far as the device (there is none here)
+        assert append(*apart) not in (0, INVALID)
+        assert read(0, 256, 1) not in (0, INVALID) and read(1024, 0, 4) not in (0, INVALID)
