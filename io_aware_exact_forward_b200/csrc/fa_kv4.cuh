@@ -789,7 +789,10 @@ fa_kv4_split_kernel(const __grid_constant__ Kv4DecodeParams p) {
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const bool move = mx > m_run + (C::RESCALE_THRESHOLD - kKv4RefAbove) || (m_run == -INFINITY && mx != -INFINITY);
       uint32_t ps[NG / 2];  // V's steps of key `lane`, scaled
-      const uint32_t at_sw = dst_p + s * C::STAGE_BYTES + (C::OFF_VP - C::OFF_KP);
+      // the same address from what is in registers anyway: 288 us against 291 at d =
+      // 128 (64 sequences of 1k to 32k keys); the other way round, 183 against 177, at 64
+      const uint32_t at_sw = D == 128 ? dst_p + s * C::STAGE_BYTES + (C::OFF_VP - C::OFF_KP)
+                                      : st + C::OFF_VP + lane * C::PB;
       kv4_steps<NG>(at_sw, ps);
       bool wide = false;
 #pragma unroll
