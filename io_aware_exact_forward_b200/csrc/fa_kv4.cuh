@@ -90,10 +90,11 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // Both kernels below take units of eight elements of one row.  A thread keeps its
 // head and its place in the row and walks along the tokens, so that indexes are
 // divided out once; a block has two heads of 8 tokens (d = 128; 16 at 64) side by
-// side, so that it meets 512 contiguous bytes on either side at a time.  They are bound by HBM (2 bytes an element on one side and
-// 0.625 on the other) and, closely behind, by issue: 32k tokens of 8 heads of 128
-// take the bytes 27 us each way; append takes 54 us (165 instructions per warp and
-// unit, half of them on the half-rate integer pipe) and read 31.  One index per unit
+// side, so that it meets 512 contiguous bytes on either side at a time.  The bytes
+// (2 an element on one side and 0.625 on the other) would take 27 us each way for
+// 32k tokens of 8 heads of 128: read takes 31.  Append takes 54, by issue and the
+// half-rate integer pipe: 165 instructions per warp and unit, 47% of them on that
+// pipe, keep it 73% busy and the issue slots 77%.  One index per unit
 // divided out in 64 bits and a division per element took 110 and 56 us, in 32 bits
 // without the divisions 64 and 45.
 struct Kv4Place {
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
 // brought to u - 8 by one exact fp16 addition or fused multiply-add, so that a
 // 32-bit word of eight codes takes one shift.  (bf16 holds one nibble of every
 // four, hence three shifts; the shifts and masks go through the half-rate integer
-// pipe, which with the instruction issue is what bounds this kernel after HBM.)
+// pipe, the busiest of this kernel.)
 // Q enters as fp16 after scaling its row by a power of two to a largest value in
 // [2^14, 2^15): a bf16 value is then exact down to 2^-31 of the row's largest, and
 // smaller ones are within 2^-39 of it.  The centres' parts are two small bf16
@@ -327,8 +328,11 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const __grid_constant_
 // whatever the lengths are.  A block's stretch of one (sequence, KV head) ends
 // in a partial result (slot: block + pair, both grow along the list), and a
 // second kernel joins them.  64 sequences of 1k to 32k keys (8 KV heads of 128,
-// 1.39 GB) take 285 us, 4.85 TB/s; the bytes alone would take 214.  What bounds it
-// then is issue: about 330 instructions per warp and 16 keys, at 0.6 a cycle.
+// 1.39 GB) take 288 us, 4.81 TB/s; the bytes alone would take 214.  What holds it
+// back then is latency: about 337 instructions per warp and 16 keys are issued at
+// 0.59 a cycle, no pipe is busy half of the time (ALU 48%, tensor 38%, FMA 37%), and
+// the largest stall is the fixed wait for the instruction before, which three warps
+// a scheduler do not cover.
 // Each warp of a block takes 32 keys of every tile through a ring of its own, which
 // all its lanes fill with 16-byte asynchronous copies: no warp waits for another
 // before a stretch ends, none is spent on loading, and a slice costs ten copies (as
@@ -397,7 +401,8 @@ struct Kv4Cfg {
   static constexpr int OFF_SCAN = OFF_PRE + (kKv4MaxSeqs + 4) * 4;
   static constexpr int SMEM_BYTES = OFF_SCAN + 64 + 1024;        // + alignment slack
   // Blocks per SM: 12 warps of 168 registers at d = 128 (285 us on 64 sequences of
-  // 1k to 32k keys; 16 of 128 take 297), 16 of 128 at d = 64 (178; 12 take 186).
+  // 1k to 32k keys where 16 of 128 took 297), 16 of 128 at d = 64 (178 where 12 took
+  // 186); 288 and 177 with V's steps scaled in shared memory.
   static constexpr int CTAS = D == 128 ? 3 : 4;
   static constexpr float RESCALE_THRESHOLD = 8.0f;
   static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "shared memory of an SM");

@@ -16,7 +16,8 @@
 // Bound by HBM: 4 bytes per element and a few operations.  32k tokens of 40 heads
 // of 128 out of a packed projection take 117 us, 5.7 TB/s; 64k tokens of 32 heads
 // of 64, half of each turned, 82 us, 6.5 TB/s.  A single step's 64 tokens take 5
-// us, the latency of a launch, the angles and one round trip to memory.
+// us alone, 3 in a row of such calls in a graph: the latency of a launch, the angles
+// and one round trip to memory.
 #pragma once
 
 #include "fa_ptx.cuh"
