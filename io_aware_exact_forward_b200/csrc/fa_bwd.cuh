@@ -771,7 +771,7 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
         // overlaps the exponentials of chunk c.  P^T (bf16 pairs) goes to
         // the first 32 columns of this warp's 64, never ahead of its loads.
         uint32_t sv[2][16];
-        uint32_t any = 0u;  // sinks: the bits that any of this key's fp16 P has (chunks 0 and 3)
+        uint32_t any = 0u;  // sinks: the bits that any of this key's fp16 P has
         tmem_ld16(tS, sv[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -799,10 +799,8 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
             if constexpr (WIN == 2) ph[e] = pack_f16x2(p0, p1);
           }
           if constexpr (WIN == 2) {
-            if (c == 0 || c == 3) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) any |= ph[e];
-            }
+            for (int e = 0; e < 8; ++e) any |= ph[e];
             tmem_st8(tS + c * 16 + 8, ph);
             tmem_st8(tS + c * 16, pk);
           } else if constexpr (DROP) {
@@ -823,8 +821,7 @@ __global__ void __maxnreg__(80) fa_bwd_dkdv_kernel(const __grid_constant__ BwdPa
           // A key that is visible, but to no query with a P of 2^-21 or more (the
           // fp16 copy's exponents 8 and up): this warp's P goes to the dS warps in
           // bf16, which the sign, of no use otherwise, tells them.  Beside a P of
-          // 2^-21 what fp16 loses, 2^-39, is nothing to the key's gradients.  Looked at
-          // are the first and last 16 columns, of which a masked key sees some.
+          // 2^-21 what fp16 loses, 2^-39, is nothing to the key's gradients.
           const bool small = !(any & 0x60006000u) && (masked ? (seen[0] | seen[1]) != 0u : true);
           if (__any_sync(0xffffffffu, small)) {
 #pragma unroll 1

@@ -360,3 +360,32 @@ def test_sink_prefill_does_not_read_behind_the_window(d, deterministic):
     ref = P.sink_backward(q, k, v, do, W, S, d ** -0.5)
     for n, x in zip(("dq", "dk", "dv"), got):
         P.check(x, *ref[n], n)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("W,S", [(16, 4), (30, 5), (300, 4)])
+def test_sink_backward_rounds_once_before_the_products(d, W, S):
+    """The error of dQ and dK as a whole is that of dS rounded to bf16 once, D from the
+    rounded O, and the result rounded: P reaches dS with more bits than bf16 has, in
+    windows of a few keys too.  A rounding to bf16 is off by 2^-8 / sqrt(3) times the root
+    mean square of 1 / mantissa, sqrt(0.541) for mantissas spread evenly in their
+    logarithm: 0.00166 of the value.  8% are left for other spreads; a second
+    rounding, of P, would add 20%."""
+    B, H, T, rho = 1, 4, 600, 2.0 ** -8 * (0.541 / 3) ** 0.5
+    q, k, v, do = _inputs(B, H, H, T, T, d, W, S)
+    c = [x.cuda() for x in (q, k, v, do)]
+    o, lse = fa.forward(*c[:3], window=W, sinks=S)
+    dq, dk, _ = fa.backward(*c[:3], o, lse, c[3], window=W, sinks=S)
+    assert fa.check() == 0
+    Q, K, V, G = (P.split_heads(x, H) for x in (q, k, v, do))
+    O, _, w, _ = P.attention(Q, K, V, P.visible(T, T, W, S), d ** -0.5)
+    ds = w * (G @ V.transpose(-1, -2) - (G * O).sum(-1, keepdim=True))
+    D2 = (G ** 2 * O ** 2).sum(-1, keepdim=True)            # of D's error, in rho
+    for got, ref, var in (
+            (dq, ds @ K, ds ** 2 @ K ** 2 + D2 * (w @ K) ** 2),
+            (dk, ds.transpose(-1, -2) @ Q,
+             (ds ** 2).transpose(-1, -2) @ Q ** 2 + (w ** 2 * D2).transpose(-1, -2) @ Q ** 2)):
+        ref, var = ref * d ** -0.5, var / d
+        err = float((P.split_heads(got, H) - ref).norm())
+        want = rho * float((ref ** 2 + var).sum() ** 0.5)
+        assert err <= 1.08 * want, (err / float(ref.norm()), want / float(ref.norm()))
