@@ -107,11 +107,11 @@ int fa_forward_window(const void* q, const void* k, const void* v, void* o, floa
  * on them.  sinks = 0 gives fa_forward_window; sinks outside [0, 1024], and with
  * sinks > 0 a scale that is not positive, are FA_ERR_INVALID_ARG.  Key tiles that
  * hold neither sinks nor any key of the windows of a block of 256 query rows are
- * not read for it.  Other arguments and errors as fa_forward_window.  V has to be finite in every 128-key tile (of keys 128 n to
- * 128 n + 127) that holds a key which any row of the same block of 256 query rows
- * sees: a masked probability is 0, and 0 times a NaN or an infinity of V is NaN, as
- * for the other prefill entry points.  Other tiles, and K where no row sees it, may
- * hold anything.
+ * not read for it.  Other arguments and errors as fa_forward_window.
+ * V has to be finite in every 128-key tile (of keys 128 n to 128 n + 127) that
+ * holds a key which any row of the same block of 256 query rows sees: a masked
+ * probability is 0, and 0 times a NaN or an infinity of V is NaN, as for the other
+ * prefill entry points.  Other tiles, and K where no row sees it, may hold anything.
  */
 int fa_forward_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
                      int B, int Hq, int Hkv, int Tq, int Tk, int d, float scale, int window,
@@ -499,11 +499,11 @@ int fa_kv4_read(void* k, void* v, const void* k_codes, const void* k_params, con
  * query does not see may hold anything.  The same inputs give the same bits.
  * LSE depends on q and K alone.  q and p times V's step are multiplied as fp16
  * with factors that follow the largest value of the row of q and, for each group
- * of V's dims, the largest step met so far: values of that group whose steps are 2^18
- * or more below it lose bits, and 2^28 below it they keep their centres alone.  A
- * NaN, an infinity or a very large value in a visible row of V stays with its group.  A row of q with a value
- * of 2^118 or more comes out non-finite.  K and V of magnitudes below 2^96 stay in
- * range whatever the number of keys.
+ * of V's dims, the largest step met so far: values of that group whose steps are
+ * 2^18 or more below it lose bits, and 2^28 below it they keep their centres
+ * alone.  A NaN, an infinity or a very large value in a visible row of V stays with
+ * its group.  A row of q with a value of 2^118 or more comes out non-finite.  K and
+ * V of magnitudes below 2^96 stay in range whatever the number of keys.
  */
 size_t fa_kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int Tk_max, int d);
 int fa_kv4_decode(const void* q, const void* k_codes, const void* k_params, const void* v_codes,
